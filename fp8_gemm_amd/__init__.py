@@ -40,7 +40,12 @@ class Plan(ctypes.Structure):
 
 SYMBOLS = ("fp8_gemm_nt", "fp8_gemm_nt_noalloc", "fp8_gemm_nt_blockscaled", "fp8_gemm_nt_channelwise",
            "fp8_grouped_gemm_masked_blockscaled", "fp8_grouped_gemm_contig_blockscaled", "fp8_grouped_gemm_masked", "fp8_grouped_gemm_contig",
-           "bf16_gemm_nt", "fp8_gemm_plan", "fp8_gemm_strerror", "fp8_gemm_abi_version")
+           "bf16_gemm_nt", "fp8_gemm_plan", "fp8_gemm_strerror", "fp8_gemm_abi_version",
+           "fp8_gemm_nt_fused", "bf16_gemm_nt_fused", "bf16_gemm_nt_fused_backward",
+           "bf16_gemm_nt_fused_backward_workspace", "fp8_gated_nt", "bf16_gated_nt", "bf16_gated_nt_backward",
+           "bf16_gated_nt_backward_workspace")
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
 def load_library(path: str = LIB_PATH):
@@ -74,6 +79,23 @@ def load_library(path: str = LIB_PATH):
     lib.fp8_gemm_plan.restype = I
     lib.fp8_gemm_strerror.argtypes = [I]
     lib.fp8_gemm_strerror.restype = ctypes.c_char_p
+    lib.fp8_gemm_nt_fused.argtypes = [P, I64, I, P, I64, I, P, I, P, I, P, I, P, I64, P, I64, I, I, I, P]
+    lib.fp8_gemm_nt_fused.restype = I
+    lib.bf16_gemm_nt_fused.argtypes = [P, I64, P, I64, P, I, P, I64, P, I64, P, I64, I, I, I, P]
+    lib.bf16_gemm_nt_fused.restype = I
+    lib.bf16_gemm_nt_fused_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, I, P, I64, P, I64, P, P, I64, I, I, I, P]
+    lib.bf16_gemm_nt_fused_backward.restype = I
+    lib.bf16_gemm_nt_fused_backward_workspace.argtypes = [I, I]
+    lib.bf16_gemm_nt_fused_backward_workspace.restype = I64
+    lib.fp8_gated_nt.argtypes = [P, I64, I, P, I64, P, I64, I, P, I, P, P, I, I, P, I64, I, I, I, P]
+    lib.fp8_gated_nt.restype = I
+    lib.bf16_gated_nt.argtypes = [P, I64, P, I64, P, I64, I, P, I64, P, P, I64, I, I, I, P]
+    lib.bf16_gated_nt.restype = I
+    lib.bf16_gated_nt_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, P, P, I64, I, P, I64, P, P, I64, P, I64,
+                                           I, I, I, P]
+    lib.bf16_gated_nt_backward.restype = I
+    lib.bf16_gated_nt_backward_workspace.argtypes = [I, I]
+    lib.bf16_gated_nt_backward_workspace.restype = I64
     lib.fp8_gemm_abi_version.argtypes = []
     lib.fp8_gemm_abi_version.restype = I
     _lib = lib
@@ -407,3 +429,287 @@ def grouped_gemm_contig_blockscaled(a, b, scale_a, scale_b, grp_idx, out=None, a
         a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(), scale_a.shape[1], scale_b.data_ptr(),
         scale_b.shape[2], grp_idx.data_ptr(), out.data_ptr(), M_total, G, N, K, _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Products with a fused epilogue and the gated feed-forward product
+# (include/fp8_gemm_fused.h).  They run on the current stream of the tensors'
+# device, which need not be the current one.
+# ---------------------------------------------------------------------------
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) on the current stream of `device`."""
+    torch = _torch()
+    index = device.index
+    if index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+        return
+    with torch.cuda.device(index):
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _same_device(device, **tensors):
+    if device.type != "cuda":
+        raise ValueError("all tensors must be on the GPU")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, a on {device}")
+
+
+def _rows(t, name, shape, dtype):
+    """Check a matrix with unit column stride and rows that do not overlap; its row stride."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor, got {list(t.shape)} {t.dtype}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows <= 1 or cols == 0:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}: row stride {t.stride(0)} below {cols}")
+    return t.stride(0)
+
+
+def _operand(t, name, K, grain):
+    """Check a K-contiguous operand; its row stride in elements (one that satisfies the library
+    where torch's is arbitrary: a single row or an empty matrix)."""
+    if t.dim() != 2 or t.shape[1] != K:
+        raise ValueError(f"{name} must be a [*, {K}] matrix, got {list(t.shape)}")
+    if K > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be K-contiguous (stride(1) == 1)")
+    if t.shape[0] <= 1 or K == 0:
+        return (K + grain - 1) // grain * grain
+    return t.stride(0)
+
+
+def _output(out, name, M, N, device):
+    """The BF16 output and its row stride: allocated with rows padded to 8 elements if not given."""
+    torch = _torch()
+    if out is None:
+        ld = (N + 7) // 8 * 8
+        out = torch.empty((M, ld), dtype=torch.bfloat16, device=device)
+        return (out if ld == N else out[:, :N]), max(ld, 8)
+    ld = _rows(out, name, (M, N), torch.bfloat16)
+    if out.device != device:
+        raise ValueError(f"{name} is on {out.device}, a on {device}")
+    return out, (ld if M > 1 else (N + 7) // 8 * 8)
+
+
+def _floats(t, name, *sizes):
+    """A contiguous float32 vector of one of `sizes` values: (pointer, values)."""
+    if t is None:
+        return None, 0
+    if t.dtype != _torch().float32 or t.numel() not in sizes or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor with {' or '.join(map(str, sizes))} element(s)")
+    return t.data_ptr(), t.numel()
+
+
+def _residual(t, M, N):
+    if t is None:
+        return None, 0
+    ld = _rows(t, "residual", (M, N), _torch().bfloat16)
+    return t.data_ptr(), ld
+
+
+def _bf16(*named):
+    torch = _torch()
+    for name, t in named:
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+
+
+def _fused_shapes(a, b, bname="b"):
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)} of a and {bname} are not [M, K] and [N, K]")
+    return a.shape[0], b.shape[0], a.shape[1]
+
+
+def gemm_nt_fused(a, b, scale_a=None, scale_b=None, bias=None, activation="none", residual=None, out=None,
+                  a_dtype=None, b_dtype=None):
+    """FP8 product with bias, activation and residual in its epilogue:
+
+        out[M, N] = bf16(act(scale_a[m] * scale_b[n] * a[m] . b[n] + bias[n]) + residual[m, n])
+
+    scale_a: float32, M elements or 1, or None (1); scale_b: float32, N elements
+    or 1, or None; bias: float32 [N] or None; activation: "none", "relu",
+    "silu", "gelu" (erf) or "gelu_tanh"; residual: bfloat16 [M, N] with any row
+    stride, or None; it may be `out` itself.
+    """
+    fa, fb = _fp8_code(a, a_dtype, "a"), _fp8_code(b, b_dtype, "b")
+    M, N, K = _fused_shapes(a, b)
+    dev = a.device
+    _same_device(dev, b=b, scale_a=scale_a, scale_b=scale_b, bias=bias, residual=residual)
+    lda, ldb = _operand(a, "a", K, 16), _operand(b, "b", K, 16)
+    sa, na = _floats(scale_a, "scale_a", M, 1)
+    sb, nb = _floats(scale_b, "scale_b", N, 1)
+    bp, _ = _floats(bias, "bias", N)
+    rp, ldr = _residual(residual, M, N)
+    out, ldd = _output(out, "out", M, N, dev)
+    _call(dev, load_library().fp8_gemm_nt_fused, a.data_ptr(), lda, fa, b.data_ptr(), ldb, fb, sa, na, sb, nb, bp,
+          _activation(activation), rp, ldr, out.data_ptr(), ldd, M, N, K)
+    return out
+
+
+def gemm_nt_bf16_fused(a, b, bias=None, activation="none", residual=None, out=None, preact=None):
+    """BF16 product with bias, activation and residual in its epilogue:
+
+        z = a[m] . b[n] + bias[n];  out[M, N] = bf16(act(z) + residual[m, n])
+
+    Arguments as for gemm_nt_fused.  preact: a float32 [M, N] tensor that
+    receives z, for gemm_nt_bf16_fused_backward, or None.
+    """
+    torch = _torch()
+    _bf16(("a", a), ("b", b))
+    M, N, K = _fused_shapes(a, b)
+    dev = a.device
+    _same_device(dev, b=b, bias=bias, residual=residual, preact=preact)
+    lda, ldb = _operand(a, "a", K, 8), _operand(b, "b", K, 8)
+    bp, _ = _floats(bias, "bias", N)
+    rp, ldr = _residual(residual, M, N)
+    pp, ldp = (None, 0) if preact is None else (preact.data_ptr(), _rows(preact, "preact", (M, N), torch.float32))
+    out, ldd = _output(out, "out", M, N, dev)
+    _call(dev, load_library().bf16_gemm_nt_fused, a.data_ptr(), lda, b.data_ptr(), ldb, bp, _activation(activation),
+          rp, ldr, out.data_ptr(), ldd, pp, ldp, M, N, K)
+    return out
+
+
+def _workspace(size, device):
+    torch = _torch()
+    if size < 0:
+        _check(size)
+    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+
+def gemm_nt_bf16_fused_backward(grad_out, a, b, activation="none", preact=None, bias_grad=False, a_grad=True,
+                                b_grad=True):
+    """Backward pass of gemm_nt_bf16_fused: (grad_a, grad_b, grad_bias) for the
+    gradient `grad_out` of its output (bfloat16 [M, N], any row stride), where
+
+        dz = grad_out * act'(preact);  grad_a = bf16(dz . b);  grad_b = bf16(dz^T . a);  grad_bias = dz summed over m
+
+    preact: the tensor that the forward call filled (None with activation
+    "none").  grad_bias is float32 [N]; what a_grad, b_grad or bias_grad
+    excludes is None.  The residual's gradient is grad_out itself.
+    """
+    torch = _torch()
+    _bf16(("grad_out", grad_out), ("a", a), ("b", b))
+    M, N, K = _fused_shapes(a, b)
+    dev = a.device
+    _same_device(dev, b=b, grad_out=grad_out, preact=preact)
+    act = _activation(activation)
+    lda, ldb = _operand(a, "a", K, 8), _operand(b, "b", K, 8)
+    ldg = _rows(grad_out, "grad_out", (M, N), torch.bfloat16)
+    if preact is None and act:
+        raise ValueError(f"activation {activation!r} needs preact")
+    pp, ldp = (None, 0) if preact is None else (preact.data_ptr(), _rows(preact, "preact", (M, N), torch.float32))
+    ga, ldga = _output(None, "grad_a", M, K, dev) if a_grad else (None, 0)
+    gb, ldgb = _output(None, "grad_b", N, K, dev) if b_grad else (None, 0)
+    gbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
+    lib = load_library()
+    ws = _workspace(lib.bf16_gemm_nt_fused_backward_workspace(M, N), dev)
+    _call(dev, lib.bf16_gemm_nt_fused_backward, grad_out.data_ptr(), ldg, a.data_ptr(), lda, b.data_ptr(), ldb, pp,
+          ldp, act, _ptr(ga), ldga, _ptr(gb), ldgb, _ptr(gbias), _ptr(ws), 0 if ws is None else ws.numel(), M, N, K)
+    return ga, gb, gbias
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def gated_nt(a, w_gate, w_up, scale_a=None, scale_gate=None, scale_up=None, activation="silu", out=None,
+             a_dtype=None, w_dtype=None):
+    """FP8 gated feed-forward product, one kernel for both projections, the
+    activation and the product:
+
+        out[M, N] = bf16(act(scale_a[m] * scale_gate[n] * a[m] . w_gate[n]) * (scale_a[m] * scale_up[n] * a[m] . w_up[n]))
+
+    w_gate, w_up: [N, K] of one FP8 dtype (for example the two halves of a
+    merged [2 N, K] weight); scales as for gemm_nt_fused, scale_gate and
+    scale_up of the same length.
+    """
+    fa, fw = _fp8_code(a, a_dtype, "a"), _fp8_code(w_gate, w_dtype, "w_gate")
+    if _fp8_code(w_up, w_dtype, "w_up") != fw:
+        raise TypeError("w_gate and w_up must have one FP8 dtype")
+    M, N, K = _fused_shapes(a, w_gate, "w_gate")
+    if tuple(w_up.shape) != (N, K):
+        raise ValueError(f"w_up is {list(w_up.shape)}, w_gate {[N, K]}")
+    dev = a.device
+    _same_device(dev, w_gate=w_gate, w_up=w_up, scale_a=scale_a, scale_gate=scale_gate, scale_up=scale_up)
+    lda, ldg, ldu = _operand(a, "a", K, 16), _operand(w_gate, "w_gate", K, 16), _operand(w_up, "w_up", K, 16)
+    sa, na = _floats(scale_a, "scale_a", M, 1)
+    sg, ng = _floats(scale_gate, "scale_gate", N, 1)
+    su, nu = _floats(scale_up, "scale_up", N, 1)
+    if sg is not None and su is not None and ng != nu:
+        raise ValueError("scale_gate and scale_up must have one length")
+    out, ldd = _output(out, "out", M, N, dev)
+    _call(dev, load_library().fp8_gated_nt, a.data_ptr(), lda, fa, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, fw,
+          sa, na, sg, su, max(ng, nu), _activation(activation), out.data_ptr(), ldd, M, N, K)
+    return out
+
+
+def _gated_preact(preact, M, N):
+    """(gate, up, row stride) of a float32 [2, M, N] tensor."""
+    if preact.dim() != 3 or preact.shape[0] != 2:
+        raise ValueError(f"preact must be a [2, {M}, {N}] tensor, got {list(preact.shape)}")
+    gate, up = preact[0], preact[1]
+    return gate, up, _rows(gate, "preact", (M, N), _torch().float32)
+
+
+def gated_nt_bf16(a, w_gate, w_up, activation="silu", out=None, preact=None):
+    """BF16 gated feed-forward product:
+
+        g = a[m] . w_gate[n];  u = a[m] . w_up[n];  out[M, N] = bf16(act(g) * u)
+
+    preact: a float32 [2, M, N] tensor that receives g and u, for
+    gated_nt_bf16_backward, or None.
+    """
+    _bf16(("a", a), ("w_gate", w_gate), ("w_up", w_up))
+    M, N, K = _fused_shapes(a, w_gate, "w_gate")
+    if tuple(w_up.shape) != (N, K):
+        raise ValueError(f"w_up is {list(w_up.shape)}, w_gate {[N, K]}")
+    dev = a.device
+    _same_device(dev, w_gate=w_gate, w_up=w_up, preact=preact)
+    lda, ldg, ldu = _operand(a, "a", K, 8), _operand(w_gate, "w_gate", K, 8), _operand(w_up, "w_up", K, 8)
+    pg, pu, ldp = (None, None, 0) if preact is None else _gated_preact(preact, M, N)
+    out, ldd = _output(out, "out", M, N, dev)
+    _call(dev, load_library().bf16_gated_nt, a.data_ptr(), lda, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
+          _activation(activation), out.data_ptr(), ldd, _ptr(pg), _ptr(pu), ldp, M, N, K)
+    return out
+
+
+def gated_nt_bf16_backward(grad_out, a, w_gate, w_up, preact, activation="silu", a_grad=True, w_grad=True):
+    """Backward pass of gated_nt_bf16: (grad_a, grad_gate, grad_up) for the
+    gradient `grad_out` of its output (bfloat16 [M, N], any row stride), where
+
+        dg = grad_out * u * act'(g);  du = grad_out * act(g)
+        grad_a = bf16(dg . w_gate + du . w_up);  grad_gate = bf16(dg^T . a);  grad_up = bf16(du^T . a)
+
+    preact: the tensor that the forward call filled.  What a_grad or w_grad
+    excludes is None.
+    """
+    torch = _torch()
+    _bf16(("grad_out", grad_out), ("a", a), ("w_gate", w_gate), ("w_up", w_up))
+    M, N, K = _fused_shapes(a, w_gate, "w_gate")
+    if tuple(w_up.shape) != (N, K):
+        raise ValueError(f"w_up is {list(w_up.shape)}, w_gate {[N, K]}")
+    dev = a.device
+    _same_device(dev, w_gate=w_gate, w_up=w_up, grad_out=grad_out, preact=preact)
+    lda, ldg, ldu = _operand(a, "a", K, 8), _operand(w_gate, "w_gate", K, 8), _operand(w_up, "w_up", K, 8)
+    ldgrad = _rows(grad_out, "grad_out", (M, N), torch.bfloat16)
+    pg, pu, ldp = _gated_preact(preact, M, N)
+    ga, ldga = _output(None, "grad_a", M, K, dev) if a_grad else (None, 0)
+    gw, ldgw = _output(None, "grad_gate", N, K, dev) if w_grad else (None, 0)
+    gu = _output(None, "grad_up", N, K, dev)[0] if w_grad else None
+    lib = load_library()
+    ws = _workspace(lib.bf16_gated_nt_backward_workspace(M, N), dev)
+    _call(dev, lib.bf16_gated_nt_backward, grad_out.data_ptr(), ldgrad, a.data_ptr(), lda, w_gate.data_ptr(), ldg,
+          w_up.data_ptr(), ldu, pg.data_ptr(), pu.data_ptr(), ldp, _activation(activation), _ptr(ga), ldga, _ptr(gw),
+          _ptr(gu), ldgw, _ptr(ws), 0 if ws is None else ws.numel(), M, N, K)
+    return ga, gw, gu

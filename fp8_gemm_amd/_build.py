@@ -3,12 +3,17 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "fp8_gemm.hip")
-DEPS = [os.path.join(HERE, "csrc", f) for f in ("kernels.hpp", "device_common.hpp")] + \
-       [os.path.join(ROOT, "include", "fp8_gemm.h")]
+CSRC = os.path.join(HERE, "csrc")
+SRC = os.path.join(CSRC, "fp8_gemm.hip")           # the plain, block-scaled, per-channel and grouped forms
+FUSED_SRCS = [os.path.join(CSRC, f) for f in ("fused_fp8.hip", "fused_bf16.hip")]
+DEPS = [os.path.join(CSRC, f) for f in ("kernels.hpp", "device_common.hpp", "fused.hpp", "fused_bf16.hpp",
+                                        "fused_host.hpp", "host_common.hpp")] + \
+       [os.path.join(ROOT, "include", f) for f in ("fp8_gemm.h", "fp8_gemm_fused.h")]
 LIB = os.path.join(HERE, "libfp8gemm.so")
 
 HIPCC_FLAGS = [
@@ -25,15 +30,24 @@ def hipcc() -> str:
 
 
 def build(force: bool = True) -> str:
-    """Compile the library.  Always recompiles when force is True."""
+    """Compile the library (its translation units side by side).  Always recompiles when force is True."""
+    srcs = [SRC] + FUSED_SRCS
     if not force and os.path.exists(LIB):
-        newest = max(os.path.getmtime(p) for p in [SRC] + DEPS)
+        newest = max(os.path.getmtime(p) for p in srcs + DEPS)
         if os.path.getmtime(LIB) >= newest:
             return LIB
-    tmp = LIB + ".tmp"
-    cmd = [hipcc()] + HIPCC_FLAGS + [SRC, "-o", tmp]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in srcs]
+        flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+
+        def compile_one(src, obj):
+            subprocess.run([hipcc()] + flags + ["-c", src, "-o", obj], check=True)
+
+        with ThreadPoolExecutor(len(srcs)) as pool:
+            list(pool.map(compile_one, srcs, objs))
+        out = LIB + ".tmp"
+        subprocess.run([hipcc()] + HIPCC_FLAGS + objs + ["-o", out], check=True)
+        os.replace(out, LIB)
     return LIB
 
 

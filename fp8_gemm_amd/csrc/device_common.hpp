@@ -168,6 +168,15 @@ __device__ __forceinline__ v16f mfma32x32x16_bf16_part(v8i a, v8i b, v16f c) {
                                                    0, 0, 0);
 }
 
+// The same for the 16x16 shape: both 16-byte parts of a fragment, one
+// v_mfma_f32_16x16x32_bf16 each.
+__device__ __forceinline__ v4f mfma16x16x64_bf16(v8i a, v8i b, v4f c) {
+    const v4i a0 = {a[0], a[1], a[2], a[3]}, a1 = {a[4], a[5], a[6], a[7]};
+    const v4i b0 = {b[0], b[1], b[2], b[3]}, b1 = {b[4], b[5], b[6], b[7]};
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a0), __builtin_bit_cast(v8bf, b0), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a1), __builtin_bit_cast(v8bf, b1), c, 0, 0, 0);
+}
+
 template <int FA, int FB>
 __device__ __forceinline__ v4f mfma16x16x128(v8i a, v8i b, v4f c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, FA, FB, 0, 0, 0, 0);

@@ -11,14 +11,13 @@
 #include <mutex>
 
 #include "../../include/fp8_gemm.h"
+#include "host_common.hpp"
 #include "kernels.hpp"
 
-namespace {
+namespace fp8g_host {
 
-using fp8g::GemmParams;
-
-thread_local char g_detail[512];
-thread_local char g_message[768];
+static thread_local char g_detail[512];
+static thread_local char g_message[768];
 
 int fail(int status, const char *fmt, ...) {
     va_list ap;
@@ -33,7 +32,33 @@ int ok() {
     return FP8G_OK;
 }
 
-constexpr int64_t kMaxRowStride = (int64_t(1) << 23) - 16;   // keeps 256 rows of offsets below 2^31
+// The code objects are built for gfx950 only.
+int check_device() {
+    static int cached[64];   // 0 unknown, 1 ok, -1 unsupported
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return fail(FP8G_ERR_UNSUPPORTED, "no HIP device");
+    if (dev >= 0 && dev < 64 && cached[dev] == 1) return FP8G_OK;
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return fail(FP8G_ERR_UNSUPPORTED, "cannot query device %d", dev);
+    const bool good = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    if (dev >= 0 && dev < 64) cached[dev] = good ? 1 : -1;
+    if (!good) return fail(FP8G_ERR_UNSUPPORTED, "device %d is %s; this library is built for gfx950 only", dev, prop.gcnArchName);
+    return FP8G_OK;
+}
+
+int launch_status(const char *what) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(FP8G_ERR_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
+    return ok();
+}
+
+}  // namespace fp8g_host
+
+namespace {
+
+using namespace fp8g_host;
+using fp8g::GemmParams;
+
 constexpr int kSwapMaxM = 64;                                  // swap-AB threshold of the dense form
 constexpr int kSwapWideMaxM = 192;                             // masked form: one pass over the weights up to here
 #ifndef SWAP_DEPTH
@@ -59,12 +84,6 @@ constexpr int kContigAlign = 128;                              // row alignment 
 #define T128_ST 3
 #define T128_BK 128
 #endif
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool dtype_ok(int d) { return d == FP8G_E4M3 || d == FP8G_E5M2; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------------------------
 // Shape-class choice.
@@ -323,28 +342,6 @@ int plan_impl(int op, int m, int n, int k, int groups, int expected_m, fp8g_plan
         return ok();
     }
     return fail(FP8G_ERR_ARG, "unknown op %d", op);
-}
-
-// ---------------------------------------------------------------------------
-// Device check: the code objects are built for gfx950 only.
-// ---------------------------------------------------------------------------
-int check_device() {
-    static int cached[64];   // 0 unknown, 1 ok, -1 unsupported
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return fail(FP8G_ERR_UNSUPPORTED, "no HIP device");
-    if (dev >= 0 && dev < 64 && cached[dev] == 1) return FP8G_OK;
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return fail(FP8G_ERR_UNSUPPORTED, "cannot query device %d", dev);
-    const bool good = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev >= 0 && dev < 64) cached[dev] = good ? 1 : -1;
-    if (!good) return fail(FP8G_ERR_UNSUPPORTED, "device %d is %s; this library is built for gfx950 only", dev, prop.gcnArchName);
-    return FP8G_OK;
-}
-
-int launch_status(const char *what) {
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fail(FP8G_ERR_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
-    return ok();
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,329 @@
+// BF16 tiled kernel with fused epilogues, for the forward product and both
+// backward products, and the kernels that form the gradients of the
+// pre-activations and of the bias.
+#pragma once
+
+#include "fused.hpp"
+
+namespace fp8g {
+
+// ---------------------------------------------------------------------------
+// BF16 tiled kernel.  BM x BN outputs per workgroup of WM x WN waves on
+// v_mfma 32x32x16, K in steps of 64 elements through a direct-to-LDS ring of
+// STAGES slots, as in ring_kernel: fragments read one K half ahead of the
+// matrix instructions, one barrier per step, the refill of a step's slot
+// spread over the second half's instructions.
+//
+// Either operand may be K-contiguous (rows of K elements: ring rows of 128
+// bytes, read with ds_read_b128) or K-strided (TA / TB: rows of the operand's
+// other dimension, one per K element: ring rows of BM or BN elements), so that
+// the backward products need no transposed copies of the weights, tokens or
+// gradients.  A K-strided fragment comes from ds_read_b64_tr_b16, which gives
+// lane i of each 16 lanes column i of a 4 x 16 block of 16-bit values: 4 K
+// elements of one row of the operand.  Four of them make the 32 bytes of a
+// lane's fragment, in the K order of the K-contiguous form.  The 32-byte
+// segments of a K-strided ring row k are stored at segment ^ 2 (k % 4): the 4
+// rows and 2 segments that half a wave reads then lie in different banks.
+//
+// Gated: blocks of 32 ring rows alternate between p.B and p.B2.
+// ---------------------------------------------------------------------------
+typedef short v4s __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v2u lds_read_tr16(const uint8_t *a) {
+    return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)a));
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool TA, bool TB, int EPI>
+__global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<EPI> p) {
+    constexpr bool GATED = EPI == EPI_GATED;
+    static_assert(!GATED || (!TA && !TB), "gated: K-contiguous operands");
+    constexpr int BK = 128, KE = BK / 2;           // a K step: bytes, elements
+    constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+    constexpr int SLOT = (BM + BN) * BK;
+    constexpr int CPA = BM / 8 / WAVES, CPB = BN / 8 / WAVES, CPW = CPA + CPB;   // 1 KB copies per wave per step
+    constexpr int RING = STAGES * SLOT;
+    constexpr int FPASS = (BM * BN * 4 + RING - 1) / RING, RW = TM / FPASS;   // epilogue passes, rows of a wave in each
+    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && CPA % 2 == 0 && CPB % 2 == 0, "copies split evenly");
+    static_assert(!GATED || (CPB == 4 && FN % 2 == 0), "gated: each wave copies rows of one matrix");
+    static_assert(STAGES >= 2 && RING <= 160 * 1024 && CPW * (STAGES - 1) < 64, "ring");
+    static_assert(RW % 32 == 0, "epilogue rows");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
+
+    constexpr int BNO = GATED ? BN / 2 : BN;       // output columns of a tile
+    int tm, tn;
+    tile_coords<false>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BNO;
+    const int rows_m = min(p.M - m0, BM), rows_n = min(p.N - n0, BNO);
+    const int y = blockIdx.y;
+    uint16_t *const d = y ? p.D2 : p.D;
+    const int nk = (p.K + KE - 1) / KE;
+
+    // ---- copies ----
+    // K-contiguous: copy qq fills ring rows 8 qq .. 8 qq + 7, lane l row l / 8,
+    // stored chunk l % 8 holding logical chunk (l % 8) ^ ring_key(row); the key
+    // depends on qq through its parity only.  K-strided: copy qq fills 512 /
+    // rows elements (2 or 4 K rows), lane l stored chunk l % (rows / 8) of row
+    // l / (rows / 8).  A lane's offset within the tile is fixed per copy; each
+    // step moves the descriptor's base and byte count.
+    const uint32_t lr = (uint32_t)lane / 8;
+    const uint32_t kc0 = (((uint32_t)lane % 8) ^ ring_key<128>(lr)) * 16u;
+    const uint32_t kc1 = (((uint32_t)lane % 8) ^ ring_key<128>(8 + lr)) * 16u;
+    auto strided_off = [&](int qq, int rows, int valid, int64_t ld) -> uint32_t {
+        const int cpr = rows / 8;                  // 16-byte chunks per ring row
+        const int k = qq * (512 / rows) + lane / cpr, pos = lane % cpr;
+        const int col = (((pos >> 1) ^ (2 * (k & 3))) * 16) + (pos & 1) * 8;
+        // (columns come in whole chunks: the caller's `valid` is rounded up to 8)
+        return col < valid ? (uint32_t)k * (uint32_t)ld + 2u * (uint32_t)col : kOobOffset;
+    };
+    uint32_t lo_a[CPA], lo_b[CPB];
+#pragma unroll
+    for (int i = 0; i < CPA; ++i) {
+        const int qq = wave * CPA + i;
+        lo_a[i] = TA ? strided_off(qq, BM, (rows_m + 7) & ~7, p.lda)
+                     : (uint32_t)(qq * 8 + (int)lr) * (uint32_t)p.lda + ((i & 1) ? kc1 : kc0);
+    }
+    const bool second = GATED && (wave & 1);       // this wave copies rows of p.B2
+    const int64_t ldb = second ? p.ldb2 : p.ldb;
+#pragma unroll
+    for (int i = 0; i < CPB; ++i) {
+        const int qq = wave * CPB + i;
+        const int row = GATED ? (qq / 8) * 32 + (qq % 4) * 8 + (int)lr : qq * 8 + (int)lr;
+        lo_b[i] = TB ? strided_off(qq, BN, (rows_n + 7) & ~7, p.ldb)
+                     : (uint32_t)row * (uint32_t)ldb + ((i & 1) ? kc1 : kc0);
+    }
+    const uint8_t *const a0 = p.A + (int64_t)y * p.a_gstride + (TA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
+    const uint8_t *const b0 = (second ? p.B2 : p.B) + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * ldb);
+    const uint8_t *const b1 = TB ? p.B2 + (int64_t)n0 * 2 : b0;   // rows of K steps from ksplit on
+    const uint32_t bytes_a = rows_bytes(rows_m, p.lda), bytes_b = rows_bytes(rows_n, ldb);
+    v4i srdA, srdB;
+    uint32_t lds_a = 0, lds_b = 0, ko0 = 0, ko1 = 0;
+    auto set_step = [&](int kd) {
+        if (TA) {
+            srdA = make_srd(a0 + (int64_t)kd * KE * p.lda, rows_bytes(min(KE, p.K - kd * KE), p.lda));
+        } else {
+            srdA = make_srd(a0 + (int64_t)kd * BK, kd < nk ? bytes_a - (uint32_t)(kd * BK) : 0u);
+        }
+        if (TB) {
+            const bool late = kd >= p.ksplit;
+            const int ks = late ? kd - p.ksplit : kd;
+            srdB = make_srd((late ? b1 : b0) + (int64_t)ks * KE * p.ldb,
+                            kd < nk ? rows_bytes(min(KE, p.krows - ks * KE), p.ldb) : 0u);
+        } else {
+            srdB = make_srd(b0 + (int64_t)kd * BK, kd < nk ? bytes_b - (uint32_t)(kd * BK) : 0u);
+        }
+        lds_a = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)(wave * CPA) * 1024u;
+        lds_b = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)BM * BK + (uint32_t)(wave * CPB) * 1024u;
+        // K-contiguous: lanes whose chunk starts at or past K
+        const int lim = 2 * (p.K - kd * KE);
+        ko0 = (int)kc0 < lim ? 0u : kOobOffset;
+        ko1 = (int)kc1 < lim ? 0u : kOobOffset;
+    };
+    auto issue_one = [&](int i) {
+        const uint32_t ko = (i & 1) ? ko1 : ko0;
+        if (i < CPA) dma16_m0(srdA, TA ? lo_a[i < CPA ? i : 0] : lo_a[i < CPA ? i : 0] + ko, lds_a + (uint32_t)i * 1024u);
+        else dma16_m0(srdB, TB ? lo_b[i < CPA ? 0 : i - CPA] : lo_b[i < CPA ? 0 : i - CPA] + ko,
+                      lds_b + (uint32_t)(i - CPA) * 1024u);
+    };
+
+    // ---- fragments: lane l carries row l % 32 of a 32-row block and, of each
+    // 32-element K half h, elements 16 (l / 32) .. + 15, in two parts of 8
+    const int lrow = lane & 31, khalf = lane >> 5;
+    const uint32_t key = ring_key<128>((uint32_t)lrow);
+    uint32_t fo[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            fo[h][j] = (uint32_t)lrow * BK + (((uint32_t)(4 * h + 2 * khalf + j) ^ key) & 7u) * 16u;
+    // K-strided: offset of block f (segments 2 f and 2 f + 1 of the wave's part)
+    const int trow = 16 * khalf + ((lane & 15) >> 2);
+    uint32_t to_a[FM], to_b[FN];
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+        to_a[f] = (uint32_t)(trow * BM * 2 + (((wm * TM / 16 + 2 * f + ((lane >> 4) & 1)) ^ (2 * (trow & 3))) * 32) + (lane & 3) * 8);
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+        to_b[f] = (uint32_t)(trow * BN * 2 + (((wn * TN / 16 + 2 * f + ((lane >> 4) & 1)) ^ (2 * (trow & 3))) * 32) + (lane & 3) * 8);
+    auto frag = [&](const uint8_t *base, bool strided, uint32_t to, int rowb, int h) -> v8i {
+        if (strided) {
+            const uint8_t *r = base + to + 32 * h * rowb;
+            const v2u p0 = lds_read_tr16(r), p1 = lds_read_tr16(r + 4 * rowb);
+            const v2u p2 = lds_read_tr16(r + 8 * rowb), p3 = lds_read_tr16(r + 12 * rowb);
+            return pack8((v4u){p0[0], p0[1], p1[0], p1[1]}, (v4u){p2[0], p2[1], p3[0], p3[1]});
+        }
+        return pack8(*reinterpret_cast<const v4u *>(base + fo[h][0]), *reinterpret_cast<const v4u *>(base + fo[h][1]));
+    };
+    // fragment q of K half h: weight block q < FN, else token block q - FN
+    auto read_frag = [&](v8i (&bf)[FN], v8i (&af)[FM], const uint8_t *slot, int h, int q) {
+        if (q < FN) bf[q < FN ? q : 0] = frag(slot + BM * BK + (TB ? 0 : (wn * TN + q * 32) * BK), TB, to_b[q < FN ? q : 0], BN * 2, h);
+        else af[q < FN ? 0 : q - FN] = frag(slot + (TA ? 0 : (wm * TM + (q - FN) * 32) * BK), TA, to_a[q < FN ? 0 : q - FN], BM * 2, h);
+    };
+
+    v16f acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = (v16f){0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+
+    // One K half of matrix instructions (all blocks' first parts, then their
+    // second parts: no instruction follows one on its own accumulator), with
+    // the next half's fragment reads and, in the second half, the refill of
+    // the step's slot spread between them.
+    constexpr int NT = FN * FM, NMF = 2 * NT, NFR = FN + FM;
+    auto half_step = [&](const v8i (&bf)[FN], const v8i (&af)[FM], v8i (&nb)[FN], v8i (&na)[FM], const uint8_t *read_slot,
+                         int read_h, int refill) {
+#pragma unroll
+        for (int t = 0; t < NMF; ++t) {
+            const int i = (t % NT) / FM, j = (t % NT) % FM;
+            if (t < NT) acc[i][j] = mfma32x32x16_bf16_part<0>(bf[i], af[j], acc[i][j]);
+            else acc[i][j] = mfma32x32x16_bf16_part<1>(bf[i], af[j], acc[i][j]);
+#pragma unroll
+            for (int q = (t * NFR) / NMF; q < ((t + 1) * NFR) / NMF; ++q) read_frag(nb, na, read_slot, read_h, q);
+            if (refill >= 0) {
+                if (t == 0) set_step(refill);
+#pragma unroll
+                for (int q = (t * CPW) / NMF; q < ((t + 1) * CPW) / NMF; ++q) issue_one(q);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    v8i f0b[FN], f0a[FM], f1b[FN], f1a[FM];
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+        set_step(s);
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) issue_one(i);
+    }
+    vmcnt_wait<CPW * (STAGES - 1)>();              // this wave's part of step 0 has landed
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < NFR; ++q) read_frag(f0b, f0a, smem, 0, q);
+    for (int kt = 0; kt < nk; ++kt) {
+        const uint8_t *cur = smem + (kt % STAGES) * SLOT;
+        const uint8_t *nxt = smem + ((kt + 1) % STAGES) * SLOT;
+        __builtin_amdgcn_sched_barrier(0);
+        half_step(f0b, f0a, f1b, f1a, cur, 1, -1);
+        vmcnt_wait<CPW * (STAGES - 2)>();          // this wave's part of step kt + 1 has landed
+        __syncthreads();                           // everyone's has; step kt's slot is no longer read
+        half_step(f1b, f1a, f0b, f0a, nxt, 0, kt + STAGES);
+    }
+    vmcnt_wait<0>();                               // drain the copies past the last step
+    __syncthreads();                               // every wave's have landed; the ring is free
+
+    // ---- epilogue: register r of a block holds weight row 8 (r / 4) +
+    // 4 (l / 32) + r % 4 and token l % 32
+#pragma unroll
+    for (int h = 0; h < FPASS; ++h) {
+        if (h) __syncthreads();                    // the staged rows have been read
+#pragma unroll
+        for (int jj = 0; jj < RW / 32; ++jj)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const v16f &c = acc[i][h * (RW / 32) + jj];
+                    stage_f32<BN>(smem, wm * RW + jj * 32 + lrow, wn * TN + i * 32 + b * 8 + khalf * 4,
+                                  (v4f){c[4 * b], c[4 * b + 1], c[4 * b + 2], c[4 * b + 3]});
+                }
+        __syncthreads();
+        fused_store_rows<BN, WM * RW, THREADS, 32>(p, smem, tid, m0, rows_m, n0, d,
+                                                   [=](int s) { return (s / RW) * TM + h * RW + s % RW; });
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the pre-activations: fused dZ = dD act'(Z), gated dG = dH U
+// act'(G) and dU = dH act(G), rounded to BF16 once, the operands of the
+// backward products, into W [M][ldw] (gated: dU from column ldw / 2 on), whose
+// columns past N hold zeros.  Bound by memory: 6 bytes read and 2 written per
+// element (fused), 10 and 4 (gated).
+// BIAS: also the column sums of the FP32 dZ over the block's rows into
+// part[block row][N], added over the rows in a fixed order.
+// A block is 32 groups of 8 columns x 8 rows of threads, kGradRows rows.
+// ---------------------------------------------------------------------------
+constexpr int kGradRows = 64;
+
+struct GradParams {
+    const uint16_t *G;         // output gradient [M][ldg] BF16
+    const float *pre, *pre2;   // pre-activations [M][ldp] (NULL: act none)
+    uint16_t *W;               // NULL: column sums only
+    float *part;
+    int64_t ldg, ldp, ldw;
+    int M, N, act, g_vec, p_vec;
+};
+
+__device__ __forceinline__ void load_f32_row8(const float *src, int nv, bool vec, float (&out)[8]) {
+    if (vec && nv >= 8) {
+        const v4f a = *reinterpret_cast<const v4f *>(src), b = *reinterpret_cast<const v4f *>(src + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { out[e] = a[e]; out[4 + e] = b[e]; }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = e < nv ? src[e] : 0.0f;
+    }
+}
+
+template <bool GATED, bool BIAS>
+__global__ __launch_bounds__(256) void grad_kernel(GradParams p) {
+    __shared__ float sums[BIAS ? 8 * 256 : 1];
+    const int tid = threadIdx.x;
+    const int n = blockIdx.y * 256 + (tid & 31) * 8;
+    const int nv = p.N - n;                        // <= 0: padding columns
+    const int half = GATED ? (int)(p.ldw / 2) : (int)p.ldw;   // columns of W per matrix
+    float bsum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int r0 = blockIdx.x * kGradRows;
+    for (int r = r0 + (tid >> 5); r < min(p.M, r0 + kGradRows); r += 8) {
+        float g[8], z[8], z2[8], dz[8], du[8];
+        load_bf16_row<8>(p.G + (int64_t)r * p.ldg + n, nv, p.g_vec, g);
+        if (p.pre) load_f32_row8(p.pre + (int64_t)r * p.ldp + n, nv, p.p_vec, z);
+        if (GATED) load_f32_row8(p.pre2 + (int64_t)r * p.ldp + n, nv, p.p_vec, z2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= nv) {                         // (a padding column is zero whatever its gradient)
+                dz[e] = du[e] = 0.0f;
+            } else if (GATED) {
+                dz[e] = g[e] * z2[e] * act_slope(p.act, z[e]);
+                du[e] = g[e] * act_value_exact(p.act, z[e]);
+            } else {
+                dz[e] = p.pre ? g[e] * act_slope(p.act, z[e]) : g[e];
+            }
+            if (BIAS) bsum[e] += dz[e];
+        }
+        if (p.W && n < half) {                     // (half is a multiple of 64: whole groups)
+            const v2u lo = pack_bf16x4(dz[0], dz[1], dz[2], dz[3]), hi = pack_bf16x4(dz[4], dz[5], dz[6], dz[7]);
+            *reinterpret_cast<v4u *>(p.W + (int64_t)r * p.ldw + n) = (v4u){lo[0], lo[1], hi[0], hi[1]};
+            if (GATED) {
+                const v2u l2 = pack_bf16x4(du[0], du[1], du[2], du[3]), h2 = pack_bf16x4(du[4], du[5], du[6], du[7]);
+                *reinterpret_cast<v4u *>(p.W + (int64_t)r * p.ldw + half + n) = (v4u){l2[0], l2[1], h2[0], h2[1]};
+            }
+        }
+    }
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[(tid >> 5) * 256 + (tid & 31) * 8 + e] = bsum[e];
+        __syncthreads();
+        float total = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) total += sums[k * 256 + tid];
+        const int c = blockIdx.y * 256 + tid;
+        if (c < p.N) p.part[(int64_t)blockIdx.x * p.N + c] = total;
+    }
+}
+
+// Column sums of part [rows][N], in row order.
+__global__ __launch_bounds__(256) void bias_grad_kernel(const float *part, int rows, int n, float *out) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= n) return;
+    float total = 0.0f;
+    for (int r = 0; r < rows; ++r) total += part[(int64_t)r * n + c];
+    out[c] = total;
+}
+
+}  // namespace fp8g

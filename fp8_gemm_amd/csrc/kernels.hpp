@@ -45,8 +45,13 @@ enum { MODE_DENSE = 0, MODE_MASKED = 1, MODE_CONTIG = 2 };
 // 128-element K block, or a scale per row of A and a scale and bias per output
 // channel applied in the epilogue.
 enum { SCALE_TENSOR = 0, SCALE_BLOCK = 1, SCALE_CHANNEL = 2 };
+// Epilogues of the tiled and few-token kernels: scale, round and store (the
+// forms of this file), or those of fused.hpp: bias, activation and residual,
+// or the gated product of two weight matrices.
+enum { EPI_STORE = 0, EPI_ACT = 1, EPI_GATED = 2 };
 
 struct GemmParams {
+    static constexpr int kEpilogue = EPI_STORE;
     const uint8_t *A;          // tokens: [m x K] rows of lda bytes (per group: + g * a_gstride)
     const uint8_t *B;          // weights: [n x K] rows of ldb bytes (per group: + g * b_gstride)
     uint16_t *D;               // BF16 [m x N], ldd elements (per group: + g * d_gstride)
@@ -75,6 +80,17 @@ struct GemmParams {
     int *cnt;
     int splits, ksteps;
 };
+
+// The fused epilogues (fused.hpp): the FP32 sums of a tile staged in LDS, row
+// by row, and then turned into outputs 8 columns at a time; or four sums of a
+// few-token lane.
+template <int BN>
+__device__ __forceinline__ void stage_f32(uint8_t *smem, int s, int col, v4f v);
+template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf>
+__device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, int tid, int m0, int rows_m, int n0,
+                                                 uint16_t *d, RowOf row_of);
+template <class P>
+__device__ __forceinline__ void fused_store4(const P &p, int m, int n, v4f a, v4f b);
 
 // Ints per arrival count of the split-K workspace: one 128-byte line each.
 constexpr int kCountStride = 32;
@@ -776,9 +792,19 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void ring_kernel(GemmParams p) {
 //   - second half: each register set takes step kt + 1's fragment as soon as
 //     its last use in step kt has issued.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int STAGES, int FA, int FB, int MODE, int SCL, bool KTAIL>
-__global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
-    constexpr bool CHN = SCL == SCALE_CHANNEL, BLK = SCL == SCALE_BLOCK;
+// Fused epilogues (P::kEpilogue, dense form without block scales): the tile's
+// FP32 sums go to fused.hpp's epilogue.  The gated form's BN weight rows are
+// two matrices' BN / 2 rows each, in alternating blocks of 16 (ring rows
+// 32 q .. + 15 hold rows 16 q .. + 15 of p.B, the next 16 the same rows of
+// p.B2), so that a lane's blocks j and j + 1 hold the two sums of the same
+// outputs; only the rows that the copies fetch differ.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int STAGES, int FA, int FB, int MODE, int SCL, bool KTAIL, class P>
+__device__ __forceinline__ void tile16_body(P p) {
+    constexpr int EPI = P::kEpilogue;
+    constexpr bool GATED = EPI == EPI_GATED;
+    constexpr bool CHN = SCL == SCALE_CHANNEL && EPI == EPI_STORE, BLK = SCL == SCALE_BLOCK;
+    static_assert(EPI == EPI_STORE || (MODE == MODE_DENSE && SCL == SCALE_CHANNEL && BN == 256), "fused epilogues");
     // The contiguous grouped form stays on ring_kernel: there, with every
     // expert's weights streaming from HBM, this kernel measured 4% slower
     // (1.90 against 1.82 ms on the 65536-row prefill).
@@ -849,20 +875,26 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
     if constexpr (MODE == MODE_CONTIG) {
         if (!place_contig_tile(p, cs, pass, spot)) continue;   // uniform over the workgroup
     } else {
-        if (!place_tile<BM, BN, MODE>(p, lane, spot)) return;
+        if (!place_tile<BM, GATED ? BN / 2 : BN, MODE>(p, lane, spot)) return;
     }
     const int m0 = spot.m0, rows_m = spot.rows_m;
-    const int n0 = spot.n0, rows_n = spot.rows_n;
+    const int n0 = spot.n0, rows_n = spot.rows_n;  // (gated: rows of each weight matrix)
     const int expert = spot.expert;
     uint64_t *const rowmask = reinterpret_cast<uint64_t *>(smem + MASK_AT);
     if constexpr (MODE == MODE_CONTIG) contig_row_mask<BM, WAVES>(p, spot, wave, lane, rowmask);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
     const uint8_t *a_base = p.A + (int64_t)m0 * p.lda;
     const uint8_t *b_base = p.B + (int64_t)expert * p.b_gstride + (int64_t)n0 * p.ldb;
-    const float sc = (CHN || BLK) ? 1.0f : p.scale_a[0] * p.scale_b[expert];
+    const float sc = SCL != SCALE_TENSOR ? 1.0f : p.scale_a[0] * p.scale_b[expert];
     // Rows past rows_m / rows_n fall outside the descriptors: zeros, no memory access.
     const v4i srdA = make_srd(a_base, rows_bytes(rows_m, p.lda));
     const v4i srdB = make_srd(b_base, rows_bytes(rows_n, p.ldb));
+    v4i srdB2 = srdB;                              // gated: the second weight matrix
+    int64_t ldb2 = p.ldb;
+    if constexpr (GATED) {
+        ldb2 = p.ldb2;
+        srdB2 = make_srd(p.B2 + (int64_t)n0 * p.ldb2, rows_bytes(rows_n, p.ldb2));
+    }
 
     // ---- copies.  Per step the tile is (BM + BN) / 8 copy instructions of 8
     // rows x 128 bytes, CPW per wave.  Copy qq of an operand fills its ring
@@ -897,8 +929,23 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
         const bool isA = UNI ? wA : i < CPA;
         const int qq = UNI ? (wave * CPW + i) % (BM / DROWS) : (isA ? wave * CPA + i : wave * CPB + (i - CPA));
         const int row = qq * DROWS + (int)lrow_in;
-        lo_q[i] = (uint32_t)(isA ? a_row(row) : row) * (uint32_t)(isA ? p.lda : p.ldb) + ((qq & 1) ? dkc1 : dkc0);
+        if constexpr (GATED) {
+            // copies 4 q, 4 q + 1 of the weights' side: rows 16 q .. + 15 of
+            // p.B, 4 q + 2 and 4 q + 3: those of p.B2
+            const int wrow = (qq / 4) * 16 + (qq & 1) * DROWS + (int)lrow_in;
+            lo_q[i] = (uint32_t)(isA ? row : wrow) * (uint32_t)(isA ? p.lda : ((qq & 2) ? ldb2 : p.ldb)) +
+                      ((qq & 1) ? dkc1 : dkc0);
+        } else {
+            lo_q[i] = (uint32_t)(isA ? a_row(row) : row) * (uint32_t)(isA ? p.lda : p.ldb) + ((qq & 1) ? dkc1 : dkc0);
+        }
     }
+    // gated: copies i with (i & 2) take the second descriptor (i and qq agree
+    // in that bit: CPW, or CPA and CPB, are multiples of 4)
+    static_assert(!GATED || (UNI ? CPW % 4 == 0 : CPA % 4 == 0 && CPB % 4 == 0), "gated copies");
+    const v4i srd0A2 = UNI ? (wA ? srdA : srdB2) : srdA;
+    const uint64_t baseA2 = ((uint64_t)(uint32_t)srd0A2[1] << 32) | (uint32_t)srd0A2[0];
+    const uint64_t baseB2 = ((uint64_t)(uint32_t)srdB2[1] << 32) | (uint32_t)srdB2[0];
+    v4i srdAk2 = srd0A2, srdBk2 = srdB2;
     const v4i srd0A = UNI ? (wA ? srdA : srdB) : srdA;
     const uint64_t baseA = ((uint64_t)(uint32_t)srd0A[1] << 32) | (uint32_t)srd0A[0];
     const uint64_t baseB = ((uint64_t)(uint32_t)srdB[1] << 32) | (uint32_t)srdB[0];
@@ -922,6 +969,18 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
         srdAk[1] = (int)(uint32_t)(ba >> 32);
         srdAk[2] = kd < nk ? srd0A[2] - kd * BK : 0;
         lds_a = lds_wa + (uint32_t)(kd % STAGES) * SLOT;
+        if (GATED && UNI) {
+            const uint64_t ba2 = baseA2 + (uint64_t)kd * BK;
+            srdAk2[0] = (int)(uint32_t)ba2;
+            srdAk2[1] = (int)(uint32_t)(ba2 >> 32);
+            srdAk2[2] = kd < nk ? srd0A2[2] - kd * BK : 0;
+        }
+        if (GATED && !UNI) {
+            const uint64_t bb2 = baseB2 + (uint64_t)kd * BK;
+            srdBk2[0] = (int)(uint32_t)bb2;
+            srdBk2[1] = (int)(uint32_t)(bb2 >> 32);
+            srdBk2[2] = kd < nk ? srdB2[2] - kd * BK : 0;
+        }
         if (!UNI) {
             const uint64_t bb = baseB + (uint64_t)kd * BK;
             srdBk[0] = (int)(uint32_t)bb;
@@ -940,8 +999,8 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
     auto issue_one = [&](int i) {
         const bool inB = FLIPB && i >= CPA;
         const uint32_t voff = KTAIL ? lo_q[i] + ((i & 1) ? (inB ? kob1 : ko1) : (inB ? kob0 : ko0)) : lo_q[i];
-        if (UNI || i < CPA) dma16_m0(srdAk, voff, lds_a + (uint32_t)i * 1024u);
-        else dma16_m0(srdBk, voff, lds_b + (uint32_t)(i - CPA) * 1024u);
+        if (UNI || i < CPA) dma16_m0(GATED && UNI && (i & 2) ? srdAk2 : srdAk, voff, lds_a + (uint32_t)i * 1024u);
+        else dma16_m0(GATED && (i & 2) ? srdBk2 : srdBk, voff, lds_b + (uint32_t)(i - CPA) * 1024u);
     };
     // BLK: every wave copies step kd's scales into the scale slot of its ring
     // slot: A's BM row scales (4 per lane) and B's scale dwords (one per
@@ -1114,7 +1173,26 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
     // The loop orders below are the ones that keep the compiler's copies of
     // the 256 accumulators out of AGPRs within the register budget (the other
     // order spills in each case).
-    if constexpr (CHN) {
+    if constexpr (EPI != EPI_STORE) {
+        // FP32 sums staged RW rows of each wave at a time, then fused.hpp's
+        // epilogue over the staged rows (see fused_store_rows)
+        constexpr int FPASS = BM * BN * 4 > SMEM ? 2 : 1, RW = TM / FPASS;
+        static_assert(BM * BN * 4 / FPASS <= SMEM, "FP32 staging fits the ring");
+#pragma unroll
+        for (int h = 0; h < FPASS; ++h) {
+            if (h) __syncthreads();                // the staged rows have been read
+#pragma unroll
+            for (int ii = 0; ii < RW / 16; ++ii) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    stage_f32<BN>(smem, wm * RW + ii * 16 + er16, wn * TN + j * 16 + ekg * 4, acc[j][h * (RW / 16) + ii]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __syncthreads();
+            fused_store_rows<BN, WM * RW, THREADS, 16>(p, smem, (int)threadIdx.x, m0, rows_m, n0, p.D,
+                                                       [=](int s) { return (s / RW) * TM + h * RW + s % RW; });
+        }
+    } else if constexpr (CHN) {
         // per token block, the row scale of this lane's row, then per weight
         // block the four channels' scales and biases, read from the copies in
         // LDS where they are used (the other loop order, and keeping a weight
@@ -1147,7 +1225,8 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
             __builtin_amdgcn_sched_barrier(0);     // one token block at a time: bounded live registers
         }
     }
-    if constexpr (!BLK) {
+    if constexpr (EPI != EPI_STORE) {
+    } else if constexpr (!BLK) {
         __syncthreads();
         const int etid = PASSES > 1 ? wave * 64 + el : tid;   // formed afresh, as above
         store_staged<BM, BN, THREADS, MODE>(p, smem, etid, spot, p.D, rowmask);
@@ -1192,6 +1271,11 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
     }
     if (PASSES > 1) __syncthreads();               // the staged tile is read out before the ring refills
     }
+}
+
+template <int BM, int BN, int STAGES, int FA, int FB, int MODE, int SCL, bool KTAIL>
+__global__ __launch_bounds__(256, 1) void tile16_kernel(GemmParams p) {
+    tile16_body<BM, BN, STAGES, FA, FB, MODE, SCL, KTAIL>(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -1495,9 +1579,19 @@ __global__ __launch_bounds__(256, 1) void swap_kernel(GemmParams p) {
 //   accumulators in AGPRs, which gave the faster loop: 7.45 against 7.74 us
 //   at M = 1, N = 4096, K = 7168); larger grids share CUs two at a time.
 // ---------------------------------------------------------------------------
-template <int WAVES, int RB, int CB, int FA, int FB, int D, int SCL, int OCC>
-__global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
+// Fused epilogues (P::kEpilogue): no split over workgroups; the waves' sums go
+// to fused.hpp's epilogue.  The gated form's RB blocks are 16 RB / 2 rows of
+// each weight matrix, in turn: block 2 q holds rows 16 q .. + 15 of p.B, block
+// 2 q + 1 the same rows of p.B2.  BF16 operands arrive with K, lda and ldb in
+// bytes: a 128-byte K step is 64 elements, two instructions per block pair.
+// ---------------------------------------------------------------------------
+template <int WAVES, int RB, int CB, int FA, int FB, int D, int SCL, class P>
+__device__ __forceinline__ void decode_body(P p) {
+    constexpr int EPI = P::kEpilogue;
+    constexpr bool GATED = EPI == EPI_GATED;
     constexpr bool BLK = SCL == SCALE_BLOCK, CHN = SCL == SCALE_CHANNEL;
+    constexpr int OUT = GATED ? 8 * RB : 16 * RB;  // output columns per workgroup
+    static_assert(!GATED || RB % 2 == 0, "gated: blocks of both matrices");
     constexpr int NB = RB + CB;                    // 16-row blocks per step: RB of weights, then CB of tokens
     constexpr int NQ = 2 * NB + (BLK ? 2 : 0);     // DMA instructions per step (8 rows x 128 B each,
                                                    // and two 256-byte scale copies)
@@ -1522,15 +1616,21 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
     // remaining kernel arguments only after the branch, a second round of
     // scalar loads that cost every launch ~0.3 us.  Unsplit, grid y counts
     // the 64-token tiles of the small-shape class.
-    const int splits = max(p.splits, 1);
+    const int splits = EPI == EPI_STORE ? max(p.splits, 1) : 1;
     const int nb = blockIdx.x;
     const int sp = splits > 1 ? (int)blockIdx.y : 0;
-    const bool live = nb < (p.N + 16 * RB - 1) / (16 * RB);
-    const int n0 = nb * 16 * RB;
-    const int rows_w = live ? min(p.N - n0, 16 * RB) : 0;
+    const bool live = nb < (p.N + OUT - 1) / OUT;
+    const int n0 = nb * OUT;
+    const int rows_w = live ? min(p.N - n0, OUT) : 0;
     // Rows past N (weights) or past M (tokens) lie outside the descriptors and
     // read zeros without touching memory.
     const v4i srdW = make_srd(p.B + (int64_t)n0 * p.ldb, rows_bytes(rows_w, p.ldb));
+    v4i srdW2 = srdW;                              // gated: the second weight matrix
+    int64_t ldb2 = p.ldb;
+    if constexpr (GATED) {
+        ldb2 = p.ldb2;
+        srdW2 = make_srd(p.B2 + (int64_t)n0 * p.ldb2, rows_bytes(rows_w, p.ldb2));
+    }
     // token tile: all M tokens (M <= 64), or 64-row tile blockIdx.y of them
     // (the small-shape class, never split over K)
     const int tm0 = splits > 1 ? 0 : (int)blockIdx.y * 64;
@@ -1554,6 +1654,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
     const uint32_t dch0 = (((uint32_t)lane & 7u) ^ ((drow >> 1) & 7u)) * 16u;         // rows 0..7
     const uint32_t dch1 = (((uint32_t)lane & 7u) ^ (((drow + 8u) >> 1) & 7u)) * 16u;  // rows 8..15
     const uint32_t w0 = drow * (uint32_t)p.ldb + dch0, w1 = (drow + 8u) * (uint32_t)p.ldb + dch1;
+    const uint32_t u0 = drow * (uint32_t)ldb2 + dch0, u1 = (drow + 8u) * (uint32_t)ldb2 + dch1;
     uint32_t t0[CB], t1[CB];
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
@@ -1582,7 +1683,13 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            const uint32_t wb = (uint32_t)(16 * b) * (uint32_t)p.ldb + k0;
+            if (GATED && (b & 1)) {
+                const uint32_t ub = (uint32_t)(8 * (b - 1)) * (uint32_t)ldb2 + k0;
+                dma16(srdW2, in0 ? u0 + ub : kOobOffset, base + 2048u * b);
+                dma16(srdW2, in1 ? u1 + ub : kOobOffset, base + 2048u * b + 1024u);
+                continue;
+            }
+            const uint32_t wb = (uint32_t)(GATED ? 8 * b : 16 * b) * (uint32_t)p.ldb + k0;
             dma16(srdW, in0 ? w0 + wb : kOobOffset, base + 2048u * b);
             dma16(srdW, in1 ? w1 + wb : kOobOffset, base + 2048u * b + 1024u);
         }
@@ -1639,6 +1746,7 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
                     if (BLK) acc[r][c] = mfma16x16x128_s<FB, FA>(wf[r], tf, acc[r][c], ssb, ssa);
+                    else if constexpr (FA == FMT_BF16) acc[r][c] = mfma16x16x64_bf16(wf[r], tf, acc[r][c]);
                     else acc[r][c] = mfma16x16x128<FB, FA>(wf[r], tf, acc[r][c]);
                 }
             }
@@ -1660,6 +1768,25 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
     // output block idx = (r, c): weight rows 16 r .. of this workgroup x token
     // block c; wave w takes blocks w, w + WAVES, ...
     constexpr int NBLK = RB * CB, PER = (NBLK + WAVES - 1) / WAVES;
+    if constexpr (EPI != EPI_STORE) {
+        // output blocks (q, c): columns 16 q .. of this workgroup x token block
+        // c; wave w takes blocks w, w + WAVES, ... (gated: both matrices' sums)
+        constexpr int QB = OUT / 16;
+        auto total = [&](int idx) {
+            v4f sum = red[idx * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) sum += red[(w * NBLK + idx) * 64 + lane];
+            return sum;
+        };
+        for (int o = wave; o < QB * CB; o += WAVES) {
+            const int q = o / CB, c = o % CB;
+            const v4f z = total((GATED ? 2 * q : q) * CB + c);
+            const v4f z2 = GATED ? total((2 * q + 1) * CB + c) : z;
+            const int tok = c * 16 + r16;
+            if (tok < rows_t) fused_store4(p, tm0 + tok, n0 + q * 16 + kg * 4, z, z2);
+        }
+        return;
+    }
     v4f sums[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -1747,6 +1874,10 @@ __global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
     }
 }
 
+template <int WAVES, int RB, int CB, int FA, int FB, int D, int SCL, int OCC>
+__global__ __launch_bounds__(64 * WAVES, OCC) void decode_kernel(GemmParams p) {
+    decode_body<WAVES, RB, CB, FA, FB, D, SCL>(p);
+}
 
 // ---------------------------------------------------------------------------
 // Few-token kernel with the waves on weight rows: the dense form with M <= 64

@@ -1,0 +1,165 @@
+"""GPU parity of the products with a fused epilogue and of the gated products.
+
+References and bounds: tests/_fused.py.  The sizes put every kernel at its
+edges: one token, token counts around each class, odd output columns, K tails,
+tiles that end inside a matrix.
+"""
+import itertools
+
+import pytest
+import torch
+
+from tests import _fused as F
+
+pytestmark = pytest.mark.gpu
+
+E4, E5, BF = torch.float8_e4m3fn, torch.float8_e5m2, torch.bfloat16
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def f():
+    import fp8_gemm_amd
+    fp8_gemm_amd.load_library()
+    return fp8_gemm_amd
+
+
+def rand(seed, *shape, dtype=BF, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).to(DEV)
+
+
+def scales(seed, n):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.rand(n, generator=g) * 1.5 + 0.5).to(DEV)
+
+
+def strided(t, extra, fill=float("nan")):
+    """The same values in rows `extra` elements longer, which hold NaN."""
+    big = torch.full((t.shape[0], t.shape[1] + extra), fill, dtype=torch.float32).to(t.dtype).to(t.device)
+    big[:, :t.shape[1]] = t
+    return big[:, :t.shape[1]]
+
+
+FP8_SHAPES = [(1, 16, 16), (1, 130, 272), (5, 33, 400), (16, 64, 128), (17, 100, 144), (33, 257, 528), (64, 48, 1040),
+              (65, 300, 272), (128, 256, 128), (130, 515, 400), (257, 260, 1168), (300, 1003, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", FP8_SHAPES)
+@pytest.mark.parametrize("kind", [(E4, E4), (E5, E4)], ids=["e4m3", "mixed"])
+def test_fused_fp8(f, M, N, K, kind):
+    a, b = rand(M + K, M, K, dtype=kind[0]), rand(N + 7 * K, N, K, dtype=kind[1], std=0.25)
+    sa, sb = scales(1, M), scales(2, N)
+    bias, res = rand(3, N, dtype=torch.float32), rand(4, M, N)
+    for i, name in enumerate(F.ACTS):
+        args = dict(scale_a=[sa, sa[:1], None][i % 3], scale_b=[sb, None, sb[:1]][i % 3],
+                    bias=bias if i % 2 else None, residual=res if i != 2 else None)
+        out = f.gemm_nt_fused(a, b, activation=name, **args)
+        _, v, tight, hw = F.fused_reference(a, b, args["scale_a"], args["scale_b"], args["bias"], name, args["residual"])
+        F.check(out, v, tight, hw, K, f"fused {name} {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("fa,fb", itertools.product((E4, E5), (E4, E5)), ids=str)
+@pytest.mark.parametrize("M", [7, 40, 200, 600])
+def test_fused_fp8_formats(f, M, fa, fb):
+    N, K = 320, 320
+    a, b = rand(1, M, K, dtype=fa), rand(2, N, K, dtype=fb)
+    out = f.gemm_nt_fused(a, b, activation="silu")
+    _, v, tight, hw = F.fused_reference(a, b, name="silu")
+    F.check(out, v, tight, hw, K, "formats")
+    wu = rand(3, N, K, dtype=fb)
+    out = f.gated_nt(a, b, wu)
+    _, _, v, tight, hw = F.gated_reference(a, b, wu)
+    F.check(out, v, tight, hw, K, "gated formats")
+
+
+@pytest.mark.parametrize("M,N,K", FP8_SHAPES)
+@pytest.mark.parametrize("kind", [(E4, E4), (E5, E4)], ids=["e4m3", "mixed"])
+def test_gated_fp8(f, M, N, K, kind):
+    a = rand(M + K, M, K, dtype=kind[0])
+    wg, wu = rand(N + 7 * K, N, K, dtype=kind[1], std=0.25), rand(N + 5 * K, N, K, dtype=kind[1], std=0.25)
+    sa, sg, su = scales(1, M), scales(2, N), scales(3, N)
+    for i, name in enumerate(F.ACTS):
+        args = [(sa, sg, su), (sa[:1], sg[:1], su[:1]), (None, None, su)][i % 3]
+        out = f.gated_nt(a, wg, wu, *args, activation=name)
+        _, _, v, tight, hw = F.gated_reference(a, wg, wu, *args, name=name)
+        F.check(out, v, tight, hw, K, f"gated {name} {M}x{N}x{K}")
+
+
+BF_SHAPES = [(1, 16, 8), (1, 130, 264), (5, 33, 200), (16, 64, 64), (33, 257, 136), (64, 48, 520), (65, 300, 136),
+             (128, 256, 64), (130, 515, 200), (257, 260, 584), (300, 1003, 72)]
+
+
+@pytest.mark.parametrize("M,N,K", BF_SHAPES)
+def test_fused_bf16(f, M, N, K):
+    a, b = rand(M + K, M, K), rand(N + 7 * K, N, K, std=0.25)
+    bias, res = rand(3, N, dtype=torch.float32), rand(4, M, N)
+    for i, name in enumerate(F.ACTS):
+        bi, r = (bias if i % 2 else None), (res if i != 2 else None)
+        pre = torch.empty((M, N), device=DEV)
+        out = f.gemm_nt_bf16_fused(a, b, bias=bi, activation=name, residual=r, preact=pre)
+        z, v, tight, hw = F.fused_reference(a, b, bias=bi, name=name, res=r)
+        F.check(out, v, tight, hw, K, f"fused {name} {M}x{N}x{K}")
+        assert ((pre.cpu().double() - z).abs() <= tight + hw).all()
+        assert torch.equal(out, f.gemm_nt_bf16_fused(a, b, bias=bi, activation=name, residual=r))
+
+
+@pytest.mark.parametrize("M,N,K", BF_SHAPES)
+def test_gated_bf16(f, M, N, K):
+    a = rand(M + K, M, K)
+    wg, wu = rand(N + 7 * K, N, K, std=0.25), rand(N + 5 * K, N, K, std=0.25)
+    for name in F.ACTS:
+        pre = torch.empty((2, M, N), device=DEV)
+        out = f.gated_nt_bf16(a, wg, wu, activation=name, preact=pre)
+        g, u, v, tight, hw = F.gated_reference(a, wg, wu, name=name)
+        F.check(out, v, tight, hw, K, f"gated {name} {M}x{N}x{K}")
+        for p, (z, S, h) in zip(pre, ((g, *F.product(a, wg)[1:]), (u, *F.product(a, wu)[1:]))):
+            assert ((p.cpu().double() - z).abs() <= 1e-5 * S + h).all()
+
+
+def grad_error(name, G, z, zerr):
+    e = G.abs() * (0.8 * zerr + 2.0 ** -19 * (1 + z.abs()))
+    if name == "relu":
+        e = e + torch.where(z.abs() <= zerr, G.abs(), torch.zeros_like(G))
+    return e if name != "none" else torch.zeros_like(G)
+
+
+@pytest.mark.parametrize("M,N,K", BF_SHAPES)
+@pytest.mark.parametrize("name", F.ACTS)
+def test_fused_bf16_backward(f, M, N, K, name):
+    a, b, G = rand(M + K, M, K), rand(N + 7 * K, N, K, std=0.25), rand(9, M, N)
+    bias = rand(3, N, dtype=torch.float32)
+    pre = torch.empty((M, N), device=DEV)
+    f.gemm_nt_bf16_fused(a, b, bias=bias, activation=name, preact=pre)
+    ga, gb, gbias = f.gemm_nt_bf16_fused_backward(G, a, b, activation=name, preact=None if name == "none" else pre,
+                                                  bias_grad=True)
+    z, _, tight, hw = F.fused_reference(a, b, bias=bias)
+    g64 = G.cpu().double()
+    dz = g64 * F.act(name, z)[1]
+    err = grad_error(name, g64, z, tight + hw)
+    F.check(ga, *F.backward_products(dz, err, b), N, f"grad_a {name}")
+    F.check(gb, *F.backward_products(dz.t(), err.t(), a), M, f"grad_b {name}")
+    # FP32 sums of M terms in an order of depth at most M / 64 + 16
+    tol = err.sum(0) + (M / 64 + 16) * 2.0 ** -24 * dz.abs().sum(0) + 2.0 ** -23 * dz.abs().sum(0)
+    assert ((gbias.cpu().double() - dz.sum(0)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M,N,K", BF_SHAPES)
+@pytest.mark.parametrize("name", F.ACTS)
+def test_gated_bf16_backward(f, M, N, K, name):
+    a, G = rand(M + K, M, K), rand(9, M, N)
+    wg, wu = rand(N + 7 * K, N, K, std=0.25), rand(N + 5 * K, N, K, std=0.25)
+    pre = torch.empty((2, M, N), device=DEV)
+    f.gated_nt_bf16(a, wg, wu, activation=name, preact=pre)
+    ga, gg, gu = f.gated_nt_bf16_backward(G, a, wg, wu, pre, activation=name)
+    (g, Sg, hg), (u, Su, hu) = F.product(a, wg), F.product(a, wu)
+    eg, eu = 1e-5 * Sg + hg, 1e-5 * Su + hu
+    g64 = G.cpu().double()
+    v, dv = F.act(name, g)
+    dp, du = g64 * u * dv, g64 * v
+    err_p = grad_error(name, g64 * u, g, eg) + 1.2 * (g64.abs() * eu)
+    err_u = g64.abs() * (1.2 * eg + 2.0 ** -19 * g.abs())
+    p, q = F.backward_products(dp, err_p, wg), F.backward_products(du, err_u, wu)
+    F.check(ga, *(x + y for x, y in zip(p, q)), N, f"grad_a {name}")
+    F.check(gg, *F.backward_products(dp.t(), err_p.t(), a), M, f"grad_gate {name}")
+    F.check(gu, *F.backward_products(du.t(), err_u.t(), a), M, f"grad_up {name}")
