@@ -229,8 +229,12 @@ __device__ __forceinline__ v2u pack_bf16x4(float a, float b, float c, float d) {
 // 4096^3 GEMM still in the L2s that write-back held the next launch for
 // ~3 us (measured: 3.6 us between back-to-back kernels ending in 32 MB of
 // plain stores, 0.8 us with sc1 stores).
+// A store of more than 8 bytes may still be reading its data registers when
+// the next instructions issue: no vector instruction may write them for two
+// wait states.  The compiler keeps that distance for its own stores but not
+// for one in assembly, hence the s_nop.
 __device__ __forceinline__ void store16_wt(void *p, v4u v) {
-    asm volatile("global_store_dwordx4 %0, %1, off sc1" : : "v"(p), "v"(v) : "memory");
+    asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" : : "v"(p), "v"(v) : "memory");
 }
 
 // Store four consecutive BF16 values of one output row starting at column n.
