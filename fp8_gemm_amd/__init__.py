@@ -43,7 +43,7 @@ SYMBOLS = ("fp8_gemm_nt", "fp8_gemm_nt_noalloc", "fp8_gemm_nt_blockscaled", "fp8
            "bf16_gemm_nt", "fp8_gemm_plan", "fp8_gemm_strerror", "fp8_gemm_abi_version",
            "fp8_gemm_nt_fused", "bf16_gemm_nt_fused", "bf16_gemm_nt_fused_backward",
            "bf16_gemm_nt_fused_backward_workspace", "fp8_gated_nt", "bf16_gated_nt", "bf16_gated_nt_backward",
-           "bf16_gated_nt_backward_workspace")
+           "bf16_gated_nt_backward_workspace", "fp8_gemm_fused_plan")
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -96,6 +96,8 @@ def load_library(path: str = LIB_PATH):
     lib.bf16_gated_nt_backward.restype = I
     lib.bf16_gated_nt_backward_workspace.argtypes = [I, I]
     lib.bf16_gated_nt_backward_workspace.restype = I64
+    lib.fp8_gemm_fused_plan.argtypes = [I, I, I, I, ctypes.POINTER(Plan)]
+    lib.fp8_gemm_fused_plan.restype = I
     lib.fp8_gemm_abi_version.argtypes = []
     lib.fp8_gemm_abi_version.restype = I
     _lib = lib
@@ -436,6 +438,14 @@ def grouped_gemm_contig_blockscaled(a, b, scale_a, scale_b, grp_idx, out=None, a
 # (include/fp8_gemm_fused.h).  They run on the current stream of the tensors'
 # device, which need not be the current one.
 # ---------------------------------------------------------------------------
+
+def fused_plan(op: int, m: int, n: int, k: int) -> Plan:
+    """Kernel choice of a fused or gated form (no launch).  op: 0 gemm_nt_fused, 1 gated_nt,
+    2 gemm_nt_bf16_fused, 3 gated_nt_bf16, 4 a BF16 backward product (m x n, reduced over k)."""
+    out = Plan()
+    _check(load_library().fp8_gemm_fused_plan(op, m, n, k, ctypes.byref(out)))
+    return out
+
 
 def _activation(name):
     try:

@@ -43,17 +43,26 @@ struct FusedArgs : GemmParams {
     int ksplit, krows;
 };
 
-template <int E>
+// SCALED: the sums take scales (FP8); BF16 sums do not.
+template <int E, bool SCALED>
 struct FusedParams : FusedArgs {
     static constexpr int kEpilogue = E;
+    static constexpr bool kScaled = SCALED;
 };
 
 // ---------------------------------------------------------------------------
 // Activations, in FP32.  x sigmoid(v) is x / (1 + exp(-v)): no cancellation at
 // either end (exp overflows to infinity for v < -88, and the quotient is then
 // -0).  The tanh form of GELU is x sigmoid(2 u), since (1 + tanh u) / 2 =
-// sigmoid(2 u); the exact form is x erfc(-x / sqrt 2) / 2, which keeps its
-// relative precision where 1 + erf would cancel.
+// sigmoid(2 u).
+// The exact form is x Phi(x), Phi the normal distribution: x Q for x < 0 and
+// x (1 - Q) otherwise, with Q = Phi(-|x|) = exp(-x^2 / 2) h(|x|), which keeps
+// its relative precision where 1 + erf would cancel.  h(x) = erfcx(x / sqrt 2)
+// / 2 is smooth and falls like 1 / x: a polynomial of degree 7 in t = 1 / (1 +
+// 0.36 x) without constant term, fitted by least squares reweighted towards
+// the largest relative error, is within 7.9e-7 of it up to x = 13.5 (past
+// which Q underflows).  erfcf, with its two branches, made the epilogue of a
+// 2048 x 4096 x 14336 product 10 us longer.
 // ---------------------------------------------------------------------------
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -64,41 +73,40 @@ __device__ __forceinline__ float sigmoid_times(float x, float v) {
     return x * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
 
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-    case ACT_NONE: return z;
-    case ACT_RELU: return z < 0.0f ? 0.0f : z;     // (NaN stays NaN)
-    case ACT_SILU: return sigmoid_times(z, z);
-    case ACT_GELU: return 0.5f * z * erfcf(-kSqrtHalf * z);
-    default: return sigmoid_times(z, kGeluC * (z + kGeluA * z * z * z));
-    }
+__device__ __forceinline__ float normal_cdf(float z) {
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.36f * __builtin_fabsf(z));
+    float h = 0.04734533f;
+    h = h * t - 0.18075425f;
+    h = h * t + 0.18230114f;
+    h = h * t + 0.02562137f;
+    h = h * t + 0.14005832f;
+    h = h * t + 0.14171051f;
+    h = h * t + 0.14371745f;
+    const float q = h * t * __expf(-0.5f * z * z);
+    return z < 0.0f ? q : 1.0f - q;
 }
 
-// act'(z).  Beyond |z| = 30 every activation here has its limit slope to FP32
-// precision; the clamp keeps z^2 and z^3 finite (0 times infinity).
-__device__ __forceinline__ float act_slope(int act, float z0) {
-    const float z = z0 > 30.0f ? 30.0f : (z0 < -30.0f ? -30.0f : z0);
-    switch (act) {
-    case ACT_NONE: return 1.0f;
-    case ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    case ACT_SILU: {
-        const float s = 1.0f / (1.0f + expf(-z));
-        return s * (1.0f + z * (1.0f - s));
-    }
-    case ACT_GELU: return 0.5f * erfcf(-kSqrtHalf * z) + kInvSqrt2Pi * z * expf(-0.5f * z * z);
-    default: {
-        const float s = 1.0f / (1.0f + expf(-kGeluC * (z + kGeluA * z * z * z)));
-        return s + z * s * (1.0f - s) * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
-    }
-    }
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;     // (NaN stays NaN)
+    else if constexpr (ACT == ACT_SILU) return sigmoid_times(z, z);
+    else if constexpr (ACT == ACT_GELU) return z * normal_cdf(z);
+    else if constexpr (ACT == ACT_GELU_TANH) return sigmoid_times(z, kGeluC * (z + kGeluA * z * z * z));
+    else return z;
 }
 
-// act(z) of the backward pass, with the full-precision exponential.
-__device__ __forceinline__ float act_value_exact(int act, float z) {
+// Calls f with the activation as a compile-time value (f(int_c<ACT>{})): the
+// choice is made once per workgroup, around whole loops.  Made per value it
+// put five activations' code into the innermost loop, and the epilogue of one
+// 256 x 256 tile took 23 us.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
     switch (act) {
-    case ACT_SILU: return z / (1.0f + expf(-z));
-    case ACT_GELU_TANH: return z / (1.0f + expf(-kGeluC * (z + kGeluA * z * z * z)));
-    default: return act_value(act, z);
+    case ACT_NONE: f(int_c<ACT_NONE>{}); break;
+    case ACT_RELU: f(int_c<ACT_RELU>{}); break;
+    case ACT_SILU: f(int_c<ACT_SILU>{}); break;
+    case ACT_GELU: f(int_c<ACT_GELU>{}); break;
+    default: f(int_c<ACT_GELU_TANH>{}); break;
     }
 }
 
@@ -149,47 +157,42 @@ __device__ __forceinline__ ColumnTerms<NV> column_terms(const P &p, int n, int n
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
         const bool in = e < nv;
-        t.s[e] = in && p.ch_sb ? p.ch_sb[(n + e) * p.sb_step] : 1.0f;
-        t.s2[e] = P::kEpilogue == EPI_GATED && in && p.ch_sb2 ? p.ch_sb2[(n + e) * p.sb_step] : 1.0f;
+        t.s[e] = P::kScaled && in && p.ch_sb ? p.ch_sb[(n + e) * p.sb_step] : 1.0f;
+        t.s2[e] = P::kScaled && P::kEpilogue == EPI_GATED && in && p.ch_sb2 ? p.ch_sb2[(n + e) * p.sb_step] : 1.0f;
         t.b[e] = P::kEpilogue == EPI_ACT && in && p.bias ? p.bias[n + e] : 0.0f;
     }
     return t;
 }
 
 // The epilogue of NV consecutive outputs of row m from column n on (z: the
-// sums; gated: z of the first matrix, z2 of the second): scales and bias, the
-// pre-activations kept for the backward pass, activation, residual or product,
-// all in FP32; `out` is rounded once by the caller.
-template <int NV, class P>
-__device__ __forceinline__ void fused_outputs(const P &p, int m, int n, int nv, const ColumnTerms<NV> &t,
-                                              float (&z)[NV], float (&z2)[NV], float (&out)[NV]) {
-    constexpr int EPI = P::kEpilogue;
-    if constexpr (EPI == EPI_STORE) {
+// sums; gated: z of the first matrix, z2 of the second; sa: the row's scale;
+// r: the residual): scales and bias, the pre-activations kept for the backward
+// pass, activation, residual or product, all in FP32; `out` is rounded once by
+// the caller.
+template <int ACT, int NV, class P>
+__device__ __forceinline__ void fused_outputs(const P &p, int m, int n, int nv, const ColumnTerms<NV> &t, float sa,
+                                              const float (&r)[NV], float (&z)[NV], float (&z2)[NV], float (&out)[NV]) {
+    constexpr bool GATED = P::kEpilogue == EPI_GATED;
 #pragma unroll
-        for (int e = 0; e < NV; ++e) out[e] = z[e];
-    } else {
-        const float sa = p.ch_sa ? p.ch_sa[(int64_t)m * p.sa_step] : 1.0f;
-#pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            z[e] = z[e] * sa * t.s[e] + t.b[e];
-            if (EPI == EPI_GATED) z2[e] = z2[e] * sa * t.s2[e];
-        }
-        if (p.pre) {
-            store_f32_row<NV>(p.pre + (int64_t)m * p.ldp + n, nv, p.p_vec, z);
-            if (EPI == EPI_GATED) store_f32_row<NV>(p.pre2 + (int64_t)m * p.ldp + n, nv, p.p_vec, z2);
-        }
-#pragma unroll
-        for (int e = 0; e < NV; ++e) out[e] = act_value(p.act, z[e]);
-        if constexpr (EPI == EPI_GATED) {
-#pragma unroll
-            for (int e = 0; e < NV; ++e) out[e] *= z2[e];
-        } else if (p.R) {
-            float r[NV];
-            load_bf16_row<NV>(p.R + (int64_t)m * p.ldr + n, nv, p.r_vec, r);
-#pragma unroll
-            for (int e = 0; e < NV; ++e) out[e] += r[e];
-        }
+    for (int e = 0; e < NV; ++e) {
+        if (P::kScaled) z[e] = z[e] * sa * t.s[e];
+        if (P::kScaled && GATED) z2[e] = z2[e] * sa * t.s2[e];
+        if (!GATED) z[e] += t.b[e];
     }
+    if (!P::kScaled && p.pre) {                   // (kept by the BF16 forms only)
+        store_f32_row<NV>(p.pre + (int64_t)m * p.ldp + n, nv, p.p_vec, z);
+        if (GATED) store_f32_row<NV>(p.pre2 + (int64_t)m * p.ldp + n, nv, p.p_vec, z2);
+    }
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+        out[e] = act_value<ACT>(z[e]);
+        out[e] = GATED ? out[e] * z2[e] : out[e] + r[e];
+    }
+}
+
+template <class P>
+__device__ __forceinline__ float row_scale(const P &p, int m) {
+    return P::kScaled && p.ch_sa ? p.ch_sa[(int64_t)m * p.sa_step] : 1.0f;
 }
 
 // Four outputs of a few-token lane: row m, columns n .. n + 3.
@@ -198,8 +201,10 @@ __device__ __forceinline__ void fused_store4(const P &p, int m, int n, v4f a, v4
     const int nv = p.N - n;
     if (nv <= 0) return;
     const ColumnTerms<4> t = column_terms<4>(p, n, nv);
-    float z[4] = {a[0], a[1], a[2], a[3]}, z2[4] = {b[0], b[1], b[2], b[3]}, o[4];
-    fused_outputs<4>(p, m, n, nv, t, z, z2, o);
+    const float sa = row_scale(p, m);
+    float z[4] = {a[0], a[1], a[2], a[3]}, z2[4] = {b[0], b[1], b[2], b[3]}, o[4], r[4] = {0, 0, 0, 0};
+    if (P::kEpilogue == EPI_ACT && p.R) load_bf16_row<4>(p.R + (int64_t)m * p.ldr + n, nv, p.r_vec, r);
+    with_activation(p.act, [&](auto act) { fused_outputs<act.value, 4>(p, m, n, nv, t, sa, r, z, z2, o); });
     store_bf16x4(p.D + (int64_t)m * p.ldd + n, 0, nv, pack_bf16x4(o[0], o[1], o[2], o[3]));
 }
 
@@ -210,61 +215,162 @@ __device__ __forceinline__ void fused_store4(const P &p, int m, int n, v4f a, v4
 // one row that a read touches, lie in different banks), as many rows as fit at
 // a time; then each thread takes 8 consecutive output columns, always the same
 // ones, of every RPI-th row.  Against an epilogue in the accumulator layout:
-// one copy of the activations' code instead of one per accumulator, column
-// terms loaded once per thread, and 16-byte accesses of whole row segments for
-// the residual, the pre-activations and the output.
+// one copy of the activations' code instead of one per accumulator, and
+// 16-byte accesses of whole row segments for the residual, the pre-activations
+// and the output (4 columns and 8 bytes per thread measured 17% slower on
+// 8192 x 14336 x 4096).
+//
+// The row scales, column scales and biases wait in LDS (copy_tile_terms, before
+// the main loop), and the residuals of the next batch of U rows are loaded
+// before this batch is computed and stored: a load after a store is answered,
+// in order, only once the write-through store has reached memory.  The first
+// batch's go out before the sums are staged (`stage`, which ends in a barrier).
 // ---------------------------------------------------------------------------
 template <int BN>
 __device__ __forceinline__ void stage_f32(uint8_t *smem, int s, int col, v4f v) {
     *reinterpret_cast<v4f *>(smem + s * (BN * 4) + (((uint32_t)col >> 2) ^ ((uint32_t)s & 15u)) * 16) = v;
 }
 
-template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf>
-__device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, int tid, int m0, int rows_m, int n0,
-                                                 uint16_t *d, RowOf row_of) {
+// Copies the tile's terms into LDS: floats [0, 256) row scales, [256, 512)
+// column scales (gated: [256, 384) the first matrix's, [384, 512) the
+// second's), [512, 768) biases, 64 of each per wave of the first four, one
+// dword per lane, asynchronously (the wait for the ring's step 0 covers them).
+// Entries past the tile's rows or columns read as zeros; absent scales are
+// ones, absent biases zeros.
+template <class P>
+__device__ __forceinline__ void copy_tile_terms(const P &p, uint8_t *terms, uint32_t lds, int wave, int lane, int m0,
+                                                int rows_m, int n0, int rows_n) {
     constexpr bool GATED = P::kEpilogue == EPI_GATED;
-    constexpr int GROUPS = (GATED ? BN / 2 : BN) / 8, RPI = THREADS / GROUPS;
-    static_assert(THREADS % GROUPS == 0 && ROWS % RPI == 0, "rows split evenly over the threads");
+    if (wave >= 4) return;
+    float *const own = reinterpret_cast<float *>(terms) + wave * 64 + lane;
+    auto copy = [&](const float *src, int step, int first, int count, int idx, int at, float absent) {
+        if (src)
+            dma4(make_srd(src + (int64_t)first * step, step ? rows_bytes(count, 4) : 4u),
+                 idx < count ? 4u * (uint32_t)(idx * step) : kOobOffset, lds + (uint32_t)(at + wave * 64) * 4u);
+        else
+            own[at] = absent;
+    };
+    const int idx = wave * 64 + lane;
+    if (P::kScaled) {
+        copy(p.ch_sa, p.sa_step, m0, rows_m, idx, 0, 1.0f);
+        if (GATED && wave >= 2) copy(p.ch_sb2, p.sb_step, n0, rows_n, idx - 128, 256, 1.0f);
+        else copy(p.ch_sb, p.sb_step, n0, rows_n, idx, 256, 1.0f);
+    }
+    if (P::kEpilogue == EPI_ACT) copy(p.bias, 1, n0, rows_n, idx, 512, 0.0f);
+}
+
+template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf, class Stage>
+__device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, const uint8_t *terms, int tid, int m0,
+                                                 int rows_m, int n0, uint16_t *d, RowOf row_of, Stage stage) {
+    constexpr int EPI = P::kEpilogue;
+    constexpr bool GATED = EPI == EPI_GATED;
+    constexpr int GROUPS = (GATED ? BN / 2 : BN) / 8, RPI = THREADS / GROUPS, NIT = ROWS / RPI;
+    // (8 waves per workgroup have half the registers each)
+    constexpr int U = THREADS == 256 ? 4 : GATED ? 1 : 2;
+    static_assert(THREADS % GROUPS == 0 && ROWS % RPI == 0 && NIT % U == 0, "rows split evenly over the threads");
     const int g = tid % GROUPS;
     const int n = n0 + 8 * g;
     const int nv = p.N - n;
+    const int s0 = tid / GROUPS;
+    // the residual of U rows as loaded (whole 16-byte chunks), or element by
+    // element at the matrix' edge and for unaligned rows
+    const bool res = EPI == EPI_ACT && p.R, whole = res && p.r_vec && nv >= 8;
+    auto load_residuals = [&](v4u (&rb)[U], int i) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = row_of(s0 + (i + u) * RPI);
+            if (whole && r < rows_m) rb[u] = *reinterpret_cast<const v4u *>(p.R + (int64_t)(m0 + r) * p.ldr + n);
+        }
+    };
+    v4u rb[2][U];
+    if constexpr (EPI == EPI_ACT) load_residuals(rb[0], 0);
+    stage();
     if (nv <= 0) return;
-    const ColumnTerms<8> t = column_terms<8>(p, n, nv);
     // first 16-byte chunk of the group's sums (gated: blocks of IB columns of
     // the two matrices alternate)
     const uint32_t c0 = GATED ? (uint32_t)((g / (IB / 8)) * (IB / 2) + (g % (IB / 8)) * 2) : (uint32_t)(2 * g);
-#pragma unroll 2
-    for (int s = tid / GROUPS; s < ROWS; s += RPI) {
-        const int r = row_of(s);
-        if (r >= rows_m) continue;
+    auto read8 = [&](int s, uint32_t c, float (&z)[8]) {
         const uint8_t *row = smem + s * (BN * 4);
-        auto read8 = [&](uint32_t c, float (&z)[8]) {
-            const v4f lo = *reinterpret_cast<const v4f *>(row + (c ^ ((uint32_t)s & 15u)) * 16);
-            const v4f hi = *reinterpret_cast<const v4f *>(row + ((c + 1) ^ ((uint32_t)s & 15u)) * 16);
+        const v4f lo = *reinterpret_cast<const v4f *>(row + (c ^ ((uint32_t)s & 15u)) * 16);
+        const v4f hi = *reinterpret_cast<const v4f *>(row + ((c + 1) ^ ((uint32_t)s & 15u)) * 16);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { z[e] = lo[e]; z[4 + e] = hi[e]; }
-        };
-        float z[8], z2[8], o[8];
-        read8(c0, z);
-        if (GATED) read8(c0 + IB / 4, z2);
-        const int m = m0 + r;
-        fused_outputs<8>(p, m, n, nv, t, z, z2, o);
+        for (int e = 0; e < 4; ++e) { z[e] = lo[e]; z[4 + e] = hi[e]; }
+    };
+    auto write8 = [&](int m, const float (&o)[8]) {
         const v2u lo = pack_bf16x4(o[0], o[1], o[2], o[3]), hi = pack_bf16x4(o[4], o[5], o[6], o[7]);
         store_chunk<MODE_DENSE>(d + (int64_t)m * p.ldd + n, (v4u){lo[0], lo[1], hi[0], hi[1]}, nv);
+    };
+    if constexpr (EPI == EPI_STORE) {
+#pragma unroll U
+        for (int i = 0; i < NIT; ++i) {
+            const int s = s0 + i * RPI, r = row_of(s);
+            float z[8];
+            read8(s, c0, z);
+            if (r < rows_m) write8(m0 + r, z);
+        }
+    } else {
+        const float *const tf = reinterpret_cast<const float *>(terms);
+        ColumnTerms<8> t;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            t.s[e] = P::kScaled ? tf[256 + 8 * g + e] : 1.0f;
+            t.s2[e] = P::kScaled && GATED ? tf[384 + 8 * g + e] : 1.0f;
+            t.b[e] = GATED ? 0.0f : tf[512 + 8 * g + e];
+        }
+        with_activation(p.act, [&](auto act) {
+            auto batch = [&](const v4u (&rb)[U], int i) {
+                float o[U][8];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int s = s0 + (i + u) * RPI, r = row_of(s);
+                    float z[8], z2[8], rv[8];
+                    read8(s, c0, z);
+                    if (GATED) read8(s, c0 + IB / 4, z2);
+                    const float sa = P::kScaled ? tf[r] : 1.0f;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) rv[e] = bf16_float((uint16_t)(rb[u][e / 2] >> (16 * (e & 1))));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) rv[e] = 0.0f;
+                        if (res && r < rows_m) load_bf16_row<8>(p.R + (int64_t)(m0 + r) * p.ldr + n, nv, false, rv);
+                    }
+                    fused_outputs<act.value, 8>(p, m0 + r, n, r < rows_m ? nv : 0, t, sa, rv, z, z2, o[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = row_of(s0 + (i + u) * RPI);
+                    if (r < rows_m) write8(m0 + r, o[u]);
+                }
+            };
+            if constexpr (EPI == EPI_ACT) {
+                static_assert(NIT % (2 * U) == 0, "pairs of batches");
+#pragma unroll 1
+                for (int i = 0; i < NIT; i += 2 * U) {
+                    load_residuals(rb[1], i + U);
+                    batch(rb[0], i);
+                    if (i + 2 * U < NIT) load_residuals(rb[0], i + 2 * U);
+                    batch(rb[1], i + U);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < NIT; i += U) batch(rb[0], i);
+            }
+        });
     }
 }
 
 // ---------------------------------------------------------------------------
 // FP8: the dense loops of kernels.hpp with a fused epilogue.
 // ---------------------------------------------------------------------------
-template <int BM, int STAGES, int FA, int FB, bool KTAIL, int EPI>
-__global__ __launch_bounds__(256, 1) void fused_tile16_kernel(FusedParams<EPI> p) {
-    tile16_body<BM, 256, STAGES, FA, FB, MODE_DENSE, SCALE_CHANNEL, KTAIL>(p);
+template <int BM, int BN, int STAGES, int FA, int FB, bool KTAIL, int EPI>
+__global__ __launch_bounds__(256, 1) void fused_tile16_kernel(FusedParams<EPI, true> p) {
+    tile16_body<BM, BN, STAGES, FA, FB, MODE_DENSE, SCALE_CHANNEL, KTAIL>(p);
 }
 
 // Few tokens, FP8 and BF16.
 template <int WAVES, int RB, int CB, int FA, int FB, int D, int EPI, int OCC>
-__global__ __launch_bounds__(64 * WAVES, OCC) void fused_decode_kernel(FusedParams<EPI> p) {
+__global__ __launch_bounds__(64 * WAVES, OCC) void fused_decode_kernel(FusedParams<EPI, FA != FMT_BF16> p) {
     decode_body<WAVES, RB, CB, FA, FB, D, SCALE_CHANNEL>(p);
 }
 

@@ -10,31 +10,41 @@ using fp8g::EPI_STORE;
 using fp8g::FMT_BF16;
 using fp8g::GradParams;
 
-// ny: products sharing one launch (grid y).
-template <bool TA, bool TB, int EPI>
-int launch_tile(const FusedArgs &a, int ny, hipStream_t s) {
-    FusedParams<EPI> p = with_epilogue<EPI>(a);
-    const int cols = EPI == EPI_GATED ? 128 : 256;
-    const int bm = tile_rows((int64_t)p.M * ny, p.N, cols);
-    p.tiles_m = (int)cdiv(p.M, bm);
-    p.tiles_n = (int)cdiv(p.N, cols);
-    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny), block(512);
-    if (bm == 128)
-        hipLaunchKernelGGL((fp8g::bf16_tile_kernel<128, 256, 2, 4, 3, TA, TB, EPI>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((fp8g::bf16_tile_kernel<256, 256, 4, 2, 2, TA, TB, EPI>), grid, block, 0, s, p);
+template <int BM, int BN, int WM, int WN, int STAGES, bool TA, bool TB, int EPI>
+int launch_shape(const FusedArgs &a, int ny, hipStream_t s) {
+    auto p = with_epilogue<EPI, false>(a);
+    p.tiles_m = (int)cdiv(p.M, BM);
+    p.tiles_n = (int)cdiv(p.N, EPI == EPI_GATED ? BN / 2 : BN);
+    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny), block(64 * WM * WN);
+    hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, WM, WN, STAGES, TA, TB, EPI>), grid, block, 0, s, p);
     return launch_status("fused BF16 tiled kernel");
+}
+
+// The tiled kernel in the shape class `c`; ny: products sharing one launch
+// (grid y).
+template <bool TA, bool TB, int EPI>
+int launch_tile(ShapeClass c, const FusedArgs &a, int ny, hipStream_t s) {
+    if (c == C_128x128) return launch_shape<128, 128, 2, 2, 4, TA, TB, EPI>(a, ny, s);
+    if (c == C_128x256) return launch_shape<128, 256, 2, 4, 3, TA, TB, EPI>(a, ny, s);
+    return launch_shape<256, 256, 4, 2, 2, TA, TB, EPI>(a, ny, s);
 }
 
 // The forward products.  The few-token kernel counts K and the operands'
 // strides in bytes, the tiled kernel K in elements.
 template <int EPI>
 int launch_forward(FusedArgs p, hipStream_t s) {
-    if (p.M <= kFewMaxM) {
+    const ShapeClass c = pick_class(p.M, p.N, p.K, 2, EPI == EPI_GATED, true);
+    if (c == C_FEW) {
         p.K *= 2;
         return launch_few_fmt<FMT_BF16, FMT_BF16, EPI>(p, s);
     }
-    return launch_tile<false, false, EPI>(p, 1, s);
+    return launch_tile<false, false, EPI>(c, p, 1, s);
+}
+
+// A backward product.
+template <bool TA, bool TB>
+int launch_backward(const FusedArgs &p, int ny, hipStream_t s) {
+    return launch_tile<TA, TB, EPI_STORE>(pick_class((int64_t)p.M * ny, p.N, p.K, 2, false, false), p, ny, s);
 }
 
 FusedArgs base_args(const void *A, int64_t lda, const void *B, int64_t ldb, void *D, int64_t ldd, int M, int N, int K) {
@@ -159,11 +169,11 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
         // workspace's dZ are zero, and B's rows past N read as zeros
         FusedArgs p = base_args(dz, ldz, B, ldb, dA, ldda, M, K, direct ? N : (int)cols);
         p.krows = N;
-        if ((st = launch_tile<false, true, EPI_STORE>(p, 1, s))) return st;
+        if ((st = launch_backward<false, true>(p, 1, s))) return st;
     }
     if (want_b) {
         FusedArgs p = base_args(dz, ldz, A, lda, dB, lddb, N, K, M);
-        if ((st = launch_tile<true, true, EPI_STORE>(p, 1, s))) return st;
+        if ((st = launch_backward<true, true>(p, 1, s))) return st;
     }
     return ok();
 }
@@ -237,13 +247,13 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
         p.B2 = static_cast<const uint8_t *>(Wu);
         p.ksplit = (int)(cols / 64);
         p.krows = N;
-        if ((st = launch_tile<false, true, EPI_STORE>(p, 1, s))) return st;
+        if ((st = launch_backward<false, true>(p, 1, s))) return st;
     }
     if (want_w) {
         FusedArgs p = base_args(w, 2 * cols, A, lda, dWg, lddw, N, K, M);
         p.D2 = static_cast<uint16_t *>(dWu);
         p.a_gstride = 2 * cols;
-        if ((st = launch_tile<true, true, EPI_STORE>(p, 2, s))) return st;
+        if ((st = launch_backward<true, true>(p, 2, s))) return st;
     }
     return ok();
 }

@@ -33,7 +33,7 @@ __device__ __forceinline__ v2u lds_read_tr16(const uint8_t *a) {
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool TA, bool TB, int EPI>
-__global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<EPI> p) {
+__global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<EPI, false> p) {
     constexpr bool GATED = EPI == EPI_GATED;
     static_assert(!GATED || (!TA && !TB), "gated: K-contiguous operands");
     constexpr int BK = 128, KE = BK / 2;           // a K step: bytes, elements
@@ -47,7 +47,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
     static_assert(!GATED || (CPB == 4 && FN % 2 == 0), "gated: each wave copies rows of one matrix");
     static_assert(STAGES >= 2 && RING <= 160 * 1024 && CPW * (STAGES - 1) < 64, "ring");
     static_assert(RW % 32 == 0, "epilogue rows");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING];
+    constexpr int TERMS = EPI == EPI_ACT ? 3 * 1024 : 0;   // (copy_tile_terms; the biases are used)
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + TERMS];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -194,6 +195,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
         }
     };
 
+    if constexpr (EPI == EPI_ACT) copy_tile_terms(p, smem + RING, lds0 + (uint32_t)RING, wave, lane, m0, rows_m, n0, rows_n);
     v8i f0b[FN], f0a[FM], f1b[FN], f1a[FM];
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
@@ -219,23 +221,62 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
 
     // ---- epilogue: register r of a block holds weight row 8 (r / 4) +
     // 4 (l / 32) + r % 4 and token l % 32
-#pragma unroll
-    for (int h = 0; h < FPASS; ++h) {
-        if (h) __syncthreads();                    // the staged rows have been read
+    auto stage = [&](auto pass) {
 #pragma unroll
         for (int jj = 0; jj < RW / 32; ++jj)
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const v16f &c = acc[i][h * (RW / 32) + jj];
+                    const v16f &c = acc[i][pass.value * (RW / 32) + jj];
                     stage_f32<BN>(smem, wm * RW + jj * 32 + lrow, wn * TN + i * 32 + b * 8 + khalf * 4,
                                   (v4f){c[4 * b], c[4 * b + 1], c[4 * b + 2], c[4 * b + 3]});
                 }
-        __syncthreads();
-        fused_store_rows<BN, WM * RW, THREADS, 32>(p, smem, tid, m0, rows_m, n0, d,
-                                                   [=](int s) { return (s / RW) * TM + h * RW + s % RW; });
+    };
+    static_assert(FPASS <= 2, "two branches below");
+#pragma unroll 1
+    for (int h = 0; h < FPASS; ++h)
+        fused_store_rows<BN, WM * RW, THREADS, 32>(
+            p, smem, smem + RING, tid, m0, rows_m, n0, d, [=](int s) { return (s / RW) * TM + h * RW + s % RW; },
+            [&] {
+                if (h == 0) {
+                    stage(int_c<0>{});
+                } else {
+                    __syncthreads();               // the staged rows have been read
+                    stage(int_c<FPASS - 1>{});
+                }
+                __syncthreads();
+            });
+}
+
+// act'(z).  Beyond |z| = 30 every activation here has its limit slope to FP32
+// precision; the clamp keeps z^2 and z^3 finite (0 times infinity).
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z0) {
+    const float z = z0 > 30.0f ? 30.0f : (z0 < -30.0f ? -30.0f : z0);
+    if constexpr (ACT == ACT_RELU) {
+        return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    } else if constexpr (ACT == ACT_SILU) {
+        const float s = 1.0f / (1.0f + expf(-z));
+        return s * (1.0f + z * (1.0f - s));
+    } else if constexpr (ACT == ACT_GELU) {
+        return 0.5f * erfcf(-kSqrtHalf * z) + kInvSqrt2Pi * z * expf(-0.5f * z * z);
+    } else if constexpr (ACT == ACT_GELU_TANH) {
+        const float s = 1.0f / (1.0f + expf(-kGeluC * (z + kGeluA * z * z * z)));
+        return s + z * s * (1.0f - s) * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    } else {
+        return 1.0f;
     }
+}
+
+// act(z) of the backward pass, with the full-precision exponential and erfc
+// (that kernel waits on memory).
+template <int ACT>
+__device__ __forceinline__ float act_value_exact(float z) {
+    if constexpr (ACT == ACT_SILU) return z / (1.0f + expf(-z));
+    else if constexpr (ACT == ACT_GELU_TANH) return z / (1.0f + expf(-kGeluC * (z + kGeluA * z * z * z)));
+    else if constexpr (ACT == ACT_GELU) return 0.5f * z * erfcf(-kSqrtHalf * z);
+    else return act_value<ACT>(z);
 }
 
 // ---------------------------------------------------------------------------
@@ -252,7 +293,7 @@ constexpr int kGradRows = 64;
 
 struct GradParams {
     const uint16_t *G;         // output gradient [M][ldg] BF16
-    const float *pre, *pre2;   // pre-activations [M][ldp] (NULL: act none)
+    const float *pre, *pre2;   // pre-activations [M][ldp] (not read with act none, ungated)
     uint16_t *W;               // NULL: column sums only
     float *part;
     int64_t ldg, ldp, ldw;
@@ -279,20 +320,21 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams p) {
     const int half = GATED ? (int)(p.ldw / 2) : (int)p.ldw;   // columns of W per matrix
     float bsum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int r0 = blockIdx.x * kGradRows;
+    with_activation(p.act, [&](auto act) {
     for (int r = r0 + (tid >> 5); r < min(p.M, r0 + kGradRows); r += 8) {
         float g[8], z[8], z2[8], dz[8], du[8];
         load_bf16_row<8>(p.G + (int64_t)r * p.ldg + n, nv, p.g_vec, g);
-        if (p.pre) load_f32_row8(p.pre + (int64_t)r * p.ldp + n, nv, p.p_vec, z);
+        if (GATED || act.value != ACT_NONE) load_f32_row8(p.pre + (int64_t)r * p.ldp + n, nv, p.p_vec, z);
         if (GATED) load_f32_row8(p.pre2 + (int64_t)r * p.ldp + n, nv, p.p_vec, z2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (e >= nv) {                         // (a padding column is zero whatever its gradient)
                 dz[e] = du[e] = 0.0f;
             } else if (GATED) {
-                dz[e] = g[e] * z2[e] * act_slope(p.act, z[e]);
-                du[e] = g[e] * act_value_exact(p.act, z[e]);
+                dz[e] = g[e] * z2[e] * act_slope<act.value>(z[e]);
+                du[e] = g[e] * act_value_exact<act.value>(z[e]);
             } else {
-                dz[e] = p.pre ? g[e] * act_slope(p.act, z[e]) : g[e];
+                dz[e] = act.value != ACT_NONE ? g[e] * act_slope<act.value>(z[e]) : g[e];
             }
             if (BIAS) bsum[e] += dz[e];
         }
@@ -305,6 +347,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams p) {
             }
         }
     }
+    });
     if constexpr (BIAS) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[(tid >> 5) * 256 + (tid & 31) * 8 + e] = bsum[e];

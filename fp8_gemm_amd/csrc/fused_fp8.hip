@@ -6,24 +6,27 @@ namespace {
 using fp8g::EPI_ACT;
 using fp8g::EPI_GATED;
 
-template <int BM, int STAGES, int FA, int FB, int EPI>
+template <int BM, int BN, int STAGES, int FA, int FB, int EPI>
 int launch_tile(const FusedArgs &a, hipStream_t s) {
-    FusedParams<EPI> p = with_epilogue<EPI>(a);
+    auto p = with_epilogue<EPI, true>(a);
     p.tiles_m = (int)cdiv(p.M, BM);
-    p.tiles_n = (int)cdiv(p.N, EPI == EPI_GATED ? 128 : 256);
+    p.tiles_n = (int)cdiv(p.N, EPI == EPI_GATED ? BN / 2 : BN);
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n)), block(256);
     if (p.K % 128)
-        hipLaunchKernelGGL((fp8g::fused_tile16_kernel<BM, STAGES, FA, FB, true, EPI>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((fp8g::fused_tile16_kernel<BM, BN, STAGES, FA, FB, true, EPI>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((fp8g::fused_tile16_kernel<BM, STAGES, FA, FB, false, EPI>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((fp8g::fused_tile16_kernel<BM, BN, STAGES, FA, FB, false, EPI>), grid, block, 0, s, p);
     return launch_status("fused tiled kernel");
 }
 
 template <int FA, int FB, int EPI>
 int launch_fmt(const FusedArgs &a, hipStream_t s) {
-    if (a.M <= kFewMaxM) return launch_few_fmt<FA, FB, EPI>(a, s);
-    if (tile_rows(a.M, a.N, EPI == EPI_GATED ? 128 : 256) == 128) return launch_tile<128, 3, FA, FB, EPI>(a, s);
-    return launch_tile<256, 2, FA, FB, EPI>(a, s);
+    switch (pick_class(a.M, a.N, a.K, 1, EPI == EPI_GATED, true)) {
+    case C_FEW: return launch_few_fmt<FA, FB, EPI>(a, s);
+    case C_128x128: return launch_tile<128, 128, 4, FA, FB, EPI>(a, s);
+    case C_128x256: return launch_tile<128, 256, 3, FA, FB, EPI>(a, s);
+    default: return launch_tile<256, 256, 2, FA, FB, EPI>(a, s);
+    }
 }
 
 template <int EPI>
@@ -37,6 +40,35 @@ int launch(int fa, int fb, const FusedArgs &a, hipStream_t s) {
 }  // namespace
 
 extern "C" {
+
+int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
+    if (!out) return fail(FP8G_ERR_NULL, "plan output pointer is NULL");
+    *out = fp8g_plan{};
+    out->k_splits = 1;
+    if (op < 0 || op > 4) return fail(FP8G_ERR_ARG, "unknown op %d", op);
+    if (op < 4) {
+        if (const int st = check_sizes(m, n, k, op < 2 ? 1 : 2)) return st;
+    } else if (m < 0 || n < 0 || k < 0) {
+        return fail(FP8G_ERR_SHAPE, "negative size (m=%d n=%d k=%d)", m, n, k);
+    }
+    if (m == 0 || n == 0) return ok();
+    const bool gated = op == 1 || op == 3;
+    const ShapeClass c = pick_class(m, n, k, op < 2 ? 1 : 2, gated, op < 4);
+    if (c == C_FEW) {
+        const FewShape f = few_shape(m, n, gated);
+        out->variant = 4;
+        out->tile_m = 16 * f.cb;
+        out->tile_n = gated ? 8 * f.rb : 16 * f.rb;
+        out->token_blocks = f.cb;
+        out->workgroups = f.workgroups;
+        return ok();
+    }
+    out->variant = c == C_128x128 ? 7 : (c == C_128x256 ? 2 : 1);
+    out->tile_m = c == C_256x256 ? 256 : 128;
+    out->tile_n = (c == C_128x128 ? 128 : 256) / (gated ? 2 : 1);
+    out->workgroups = cdiv(m, out->tile_m) * cdiv(n, out->tile_n);
+    return ok();
+}
 
 int fp8_gemm_nt_fused(const void *A, int64_t lda, int a_dtype, const void *B, int64_t ldb, int b_dtype,
                       const float *scale_a, int scale_a_n, const float *scale_b, int scale_b_n, const float *bias,

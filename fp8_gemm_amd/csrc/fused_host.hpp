@@ -14,11 +14,9 @@ using namespace fp8g_host;
 using fp8g::FusedArgs;
 using fp8g::FusedParams;
 
-constexpr int kFewMaxM = 64;                       // few-token kernel up to here
-
-template <int E>
-FusedParams<E> with_epilogue(const FusedArgs &a) {
-    FusedParams<E> p = {};
+template <int E, bool SCALED>
+FusedParams<E, SCALED> with_epilogue(const FusedArgs &a) {
+    FusedParams<E, SCALED> p = {};
     static_cast<FusedArgs &>(p) = a;
     return p;
 }
@@ -80,19 +78,90 @@ int check_scale(const char *name, const float *ptr, int n, int rows, int *step) 
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens (M <= 64; larger M in tiles of 64, grid y): 16 RB weight rows per
-// workgroup of 4 waves (gated: 8 RB of each matrix).
+// Shape classes: the few-token kernel (tokens in blocks of 16, 32 or 64, grid
+// y over the 64-token tiles) and the tiled kernels of 128 x 128, 128 x 256 and
+// 256 x 256 ring rows (gated: half as many output columns).
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 4;
+enum ShapeClass { C_FEW, C_128x128, C_128x256, C_256x256 };
 
+struct FewShape {
+    int rb, cb;                // 16-row weight blocks and 16-token blocks per workgroup
+    int64_t workgroups;
+};
+
+constexpr int kFewWaves = 4;
+constexpr int few_slots(int rb, int cb) { return rb == 1 && cb == 1 ? 3 : 2; }
+
+// Twice the weight rows per workgroup where that still leaves two workgroups
+// per CU: half the token copies per weight row.
+FewShape few_shape(int64_t M, int64_t N, bool gated) {
+    FewShape f;
+    const int r0 = gated ? 2 : 1;
+    f.rb = cdiv(N, gated ? 16 : 32) >= 512 ? 2 * r0 : r0;
+    f.cb = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+    f.workgroups = cdiv(N, gated ? 8 * f.rb : 16 * f.rb) * cdiv(M, 64);
+    return f;
+}
+
+// The class with the smallest estimated time in us.  A tiled kernel's: a
+// launch, and per wave of 256 workgroups (one per CU) a fixed part (prologue
+// and epilogue) and its 128-byte K steps, each the slower the more CUs work
+// (clock and memory); the few-token kernel's: its rounds of workgroups, each a
+// fixed part shared by the workgroups that fit a CU and the bytes that its
+// copies bring in; all of them at least the time that memory takes for the
+// operands and the output.  The constants are fitted to 648 measured cases
+// (M 33 .. 4096 by nine N x K from 512 x 512 to 28672 x 512 and 1024 x 16384,
+// FP8 and BF16, fused, gated and both backward products, all four classes
+// each): on average the choice takes 0.5% longer than the fastest class.
+// Some: 512 x 4096 x 4096 FP8 38.4 / 17.7 / 29.1 / 45.6 us in the order of the
+// classes, 128 x 4096 x 4096 12.2 / 16.3 / 28.4 / 41.8, 2048 x 4096 x 4096
+// - / 43.1 / 34.9 / 47.7, 4096 x 4096 x 4096 - / 80.0 / 66.8 / 56.0.
+struct ClassCost {
+    double launch, wave, step, load;
+};
+constexpr ClassCost kCost[2][3] = {{{1.8, 3.8, 0.29, 0.14}, {1.4, 6.1, 0.60, 0.15}, {0.1, 11.0, 0.93, 0.21}},
+                                   {{1.6, 4.1, 0.335, 0.144}, {0.9, 5.3, 0.58, 0.255}, {-0.7, 9.5, 0.97, 0.39}}};
+constexpr int64_t kFewMaxM = 512;
+
+// unit: bytes per element; few: the few-token kernel is a choice.
+ShapeClass pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated, bool few) {
+    const double kbytes = (double)K * unit;
+    const int64_t cols = gated ? 2 * N : N;
+    const double memory = 2.0 + (kbytes * ((double)cols + (double)M) + 2.0 * (double)M * (double)N) / 6.0e6;
+    auto floored = [&](double t) { return (t > memory ? t : memory) + 0.05 * t; };
+    ShapeClass best = C_256x256;
+    double least = 1e300;
+    const int64_t rows[3] = {128, 128, 256}, width[3] = {128, 256, 256};
+    for (int c = 0; c < 3; ++c) {
+        const int64_t wgs = cdiv(M, rows[c]) * cdiv(cols, width[c]);
+        const ClassCost &k = kCost[unit - 1][c];
+        const double full = wgs < 256 ? (double)wgs / 256.0 : 1.0;
+        const double t = floored(k.launch + (double)cdiv(wgs, 256) *
+                                                (k.wave + (double)cdiv(K * unit, 128) * (k.step + k.load * full)));
+        if (t < least) least = t, best = (ShapeClass)(C_128x128 + c);
+    }
+    if (few && M <= kFewMaxM) {
+        const FewShape f = few_shape(M, N, gated);
+        int fit = 160 * 1024 / (kFewWaves * (f.rb + f.cb) * 2048 * few_slots(f.rb, f.cb));
+        if (fit > 3) fit = 3;
+        double rounds = fit == 1 ? (double)cdiv(f.workgroups, 256) : (double)f.workgroups / 256.0;
+        if (rounds < 1.0) rounds = 1.0;
+        if (floored(2.0 + rounds * (3.0 / fit + 16.0 * (f.rb + f.cb) * kbytes / 85e3)) <= least) best = C_FEW;
+    }
+    return best;
+}
+
+// ---------------------------------------------------------------------------
+// Few-token launch: 16 RB weight rows per workgroup of 4 waves (gated: 8 RB of
+// each matrix).
+// ---------------------------------------------------------------------------
 template <int RB, int CB, int FA, int FB, int EPI>
-int launch_few(const FusedArgs &a, hipStream_t s) {
-    constexpr int D = RB == 1 && CB == 1 ? 3 : 2;
-    constexpr int out = EPI == fp8g::EPI_GATED ? 8 * RB : 16 * RB;
-    const FusedParams<EPI> p = with_epilogue<EPI>(a);
-    const dim3 grid((unsigned)cdiv(p.N, out), (unsigned)cdiv(p.M, 64));
-    const dim3 block(64 * kFewWaves);
-    if ((int64_t)grid.x * grid.y <= 256)
+int launch_few(const FusedArgs &a, int64_t workgroups, hipStream_t s) {
+    const auto p = with_epilogue<EPI, FA != fp8g::FMT_BF16>(a);
+    const unsigned tiles = (unsigned)cdiv(p.M, 64);
+    const dim3 grid((unsigned)(workgroups / tiles), tiles), block(64 * kFewWaves);
+    constexpr int D = few_slots(RB, CB);
+    if (workgroups <= 256)
         hipLaunchKernelGGL((fp8g::fused_decode_kernel<kFewWaves, RB, CB, FA, FB, D, EPI, 1>), grid, block, 0, s, p);
     else
         hipLaunchKernelGGL((fp8g::fused_decode_kernel<kFewWaves, RB, CB, FA, FB, D, EPI, 2>), grid, block, 0, s, p);
@@ -100,26 +169,18 @@ int launch_few(const FusedArgs &a, hipStream_t s) {
 }
 
 template <int RB, int FA, int FB, int EPI>
-int launch_few_cb(const FusedArgs &a, hipStream_t s) {
-    if (a.M <= 16) return launch_few<RB, 1, FA, FB, EPI>(a, s);
-    if (a.M <= 32) return launch_few<RB, 2, FA, FB, EPI>(a, s);
-    return launch_few<RB, 4, FA, FB, EPI>(a, s);
+int launch_few_rb(const FusedArgs &a, const FewShape &f, hipStream_t s) {
+    if (f.cb == 1) return launch_few<RB, 1, FA, FB, EPI>(a, f.workgroups, s);
+    if (f.cb == 2) return launch_few<RB, 2, FA, FB, EPI>(a, f.workgroups, s);
+    return launch_few<RB, 4, FA, FB, EPI>(a, f.workgroups, s);
 }
 
 template <int FA, int FB, int EPI>
 int launch_few_fmt(const FusedArgs &a, hipStream_t s) {
     constexpr int R0 = EPI == fp8g::EPI_GATED ? 2 : 1;
-    const int64_t wide = EPI == fp8g::EPI_GATED ? cdiv(a.N, 16) : cdiv(a.N, 32);
-    if (wide >= 512) return launch_few_cb<2 * R0, FA, FB, EPI>(a, s);
-    return launch_few_cb<R0, FA, FB, EPI>(a, s);
-}
-
-// The tile rows of the 256-column tiled kernels, by the same estimate as the
-// plain dense forms: waves of 256 workgroups times the cost of a tile.
-int tile_rows(int64_t M, int64_t cols, int64_t tile_cols) {
-    const double c256 = (double)cdiv(cdiv(M, 256) * cdiv(cols, tile_cols), 256) * 2.0;
-    const double c128 = (double)cdiv(cdiv(M, 128) * cdiv(cols, tile_cols), 256) * 1.15;
-    return c128 < c256 ? 128 : 256;
+    const FewShape f = few_shape(a.M, a.N, EPI == fp8g::EPI_GATED);
+    if (f.rb == R0) return launch_few_rb<R0, FA, FB, EPI>(a, f, s);
+    return launch_few_rb<2 * R0, FA, FB, EPI>(a, f, s);
 }
 
 }  // namespace

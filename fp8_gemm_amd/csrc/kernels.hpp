@@ -84,11 +84,18 @@ struct GemmParams {
 // The fused epilogues (fused.hpp): the FP32 sums of a tile staged in LDS, row
 // by row, and then turned into outputs 8 columns at a time; or four sums of a
 // few-token lane.
+template <int I>
+struct int_c {
+    static constexpr int value = I;
+};
 template <int BN>
 __device__ __forceinline__ void stage_f32(uint8_t *smem, int s, int col, v4f v);
-template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf>
-__device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, int tid, int m0, int rows_m, int n0,
-                                                 uint16_t *d, RowOf row_of);
+template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf, class Stage>
+__device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, const uint8_t *terms, int tid, int m0,
+                                                 int rows_m, int n0, uint16_t *d, RowOf row_of, Stage stage);
+template <class P>
+__device__ __forceinline__ void copy_tile_terms(const P &p, uint8_t *terms, uint32_t lds, int wave, int lane, int m0,
+                                                int rows_m, int n0, int rows_n);
 template <class P>
 __device__ __forceinline__ void fused_store4(const P &p, int m, int n, v4f a, v4f b);
 
@@ -804,7 +811,9 @@ __device__ __forceinline__ void tile16_body(P p) {
     constexpr int EPI = P::kEpilogue;
     constexpr bool GATED = EPI == EPI_GATED;
     constexpr bool CHN = SCL == SCALE_CHANNEL && EPI == EPI_STORE, BLK = SCL == SCALE_BLOCK;
-    static_assert(EPI == EPI_STORE || (MODE == MODE_DENSE && SCL == SCALE_CHANNEL && BN == 256), "fused epilogues");
+    static_assert(EPI == EPI_STORE || (MODE == MODE_DENSE && SCL == SCALE_CHANNEL && BN != 224 && BN != 192),
+                  "fused epilogues");
+    constexpr bool SMALL = BM == 128 && BN == 128;  // (fused epilogues only)
     // The contiguous grouped form stays on ring_kernel: there, with every
     // expert's weights streaming from HBM, this kernel measured 4% slower
     // (1.90 against 1.82 ms on the 65536-row prefill).
@@ -824,11 +833,11 @@ __device__ __forceinline__ void tile16_body(P p) {
     // step's K block of each 128-row block of B (from byte 256).
     constexpr int SCS = BLK ? 512 : 0;
     constexpr int RING = STAGES * (SLOT + SCS);
-    constexpr int MASK_AT = RING > STAGE_OUT ? RING : STAGE_OUT;   // contiguous form: the tile's row mask
+    constexpr int MASK_AT = RING > STAGE_OUT || EPI != EPI_STORE ? RING : STAGE_OUT;   // contiguous form: the tile's row mask
     // per-channel form: the tile's row scales, channel scales and biases
     // (256 floats each), copied at the start, read by the epilogue
     constexpr int CH_AT = MASK_AT + (MODE == MODE_CONTIG ? BM / 8 : 0);
-    constexpr int SMEM = CH_AT + (CHN ? 3 * 1024 : 0);
+    constexpr int SMEM = CH_AT + (CHN || EPI != EPI_STORE ? 3 * 1024 : 0);
     constexpr int THREADS = 64 * WAVES;
     constexpr int OCH = BN / 8;
     constexpr int HALF = FN * FM / 2;              // MFMAs per half step
@@ -837,9 +846,9 @@ __device__ __forceinline__ void tile16_body(P p) {
     // than up to 48 at 4096^3 and 8192 x 4096 x 4096 on one box, 1.0-1.5% on a
     // slower one, where up to 40 was 2.6% slower; the contiguous form, whose
     // weights come from HBM, keeps 48, having measured 0.7% slower at 58)
-    constexpr int kBarAt = BM == 128 ? 10 : (BN == 192 ? 18 : 20), kDmaFrom = kBarAt,
-                  kDmaTo = BM == 128 ? 28 : (BN == 192 ? 46 : (BN == 256 && MODE == MODE_DENSE ? 58 : 48));
-    static_assert(((BM == 256 && (BN == 256 || BN == 224 || BN == 192)) || (BM == 128 && BN == 256)) &&
+    constexpr int kBarAt = SMALL ? 6 : BM == 128 ? 10 : (BN == 192 ? 18 : 20), kDmaFrom = kBarAt,
+                  kDmaTo = SMALL ? 16 : BM == 128 ? 28 : (BN == 192 ? 46 : (BN == 256 && MODE == MODE_DENSE ? 58 : 48));
+    static_assert(((BM == 256 && (BN == 256 || BN == 224 || BN == 192)) || (BM == 128 && BN == 256) || (SMALL && EPI != EPI_STORE)) &&
                       FN >= FM / 2 && CPA % 2 == 0, "shape");
     // block scales: each wave's weight rows must lie in one 128-row scale block
     static_assert(!BLK || BN == 256, "block scales: 256-column tiles");
@@ -1115,6 +1124,7 @@ __device__ __forceinline__ void tile16_body(P p) {
     // Entries past M or N (and absent arrays) read as zeros; the epilogue then
     // reads them from LDS instead of waiting on global loads per weight block
     // at the end of the kernel.
+    if constexpr (EPI != EPI_STORE) copy_tile_terms(p, smem + CH_AT, lds0 + (uint32_t)CH_AT, wave, lane, m0, rows_m, n0, rows_n);
     if constexpr (CHN) {
         // an absent array of scales is written as ones instead (an absent
         // bias reads zeros through an empty descriptor)
@@ -1176,22 +1186,42 @@ __device__ __forceinline__ void tile16_body(P p) {
     if constexpr (EPI != EPI_STORE) {
         // FP32 sums staged RW rows of each wave at a time, then fused.hpp's
         // epilogue over the staged rows (see fused_store_rows)
-        constexpr int FPASS = BM * BN * 4 > SMEM ? 2 : 1, RW = TM / FPASS;
-        static_assert(BM * BN * 4 / FPASS <= SMEM, "FP32 staging fits the ring");
+        constexpr int FPASS = BM * BN * 4 > RING ? 2 : 1, RW = TM / FPASS;
+        static_assert(BM * BN * 4 / FPASS <= RING && CH_AT >= RING, "FP32 staging fits the ring");
+        // (pinned to AGPRs at the loop's exit: without this the 128-row build
+        // carries the sums in VGPRs around the loop and copies all 128 of them
+        // to AGPRs and back in every K step, 121 against 97 us at 2048 x 4096
+        // x 14336)
 #pragma unroll
-        for (int h = 0; h < FPASS; ++h) {
-            if (h) __syncthreads();                // the staged rows have been read
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) asm volatile("" : "+a"(acc[j][i]));
+        auto stage = [&](auto pass) {
 #pragma unroll
             for (int ii = 0; ii < RW / 16; ++ii) {
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    stage_f32<BN>(smem, wm * RW + ii * 16 + er16, wn * TN + j * 16 + ekg * 4, acc[j][h * (RW / 16) + ii]);
+                    stage_f32<BN>(smem, wm * RW + ii * 16 + er16, wn * TN + j * 16 + ekg * 4,
+                                  acc[j][pass.value * (RW / 16) + ii]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            __syncthreads();
-            fused_store_rows<BN, WM * RW, THREADS, 16>(p, smem, (int)threadIdx.x, m0, rows_m, n0, p.D,
-                                                       [=](int s) { return (s / RW) * TM + h * RW + s % RW; });
-        }
+        };
+        // (one copy of the epilogue's code for both passes: 70 KB of it ran
+        // out of the instruction cache)
+#pragma unroll 1
+        for (int h = 0; h < FPASS; ++h)
+            fused_store_rows<BN, WM * RW, THREADS, 16>(
+                p, smem, smem + CH_AT, (int)threadIdx.x, m0, rows_m, n0, p.D,
+                [=](int s) { return (s / RW) * TM + h * RW + s % RW; },
+                [&] {
+                    if (h == 0) {
+                        stage(int_c<0>{});
+                    } else {
+                        __syncthreads();           // the staged rows have been read
+                        stage(int_c<FPASS - 1>{});
+                    }
+                    __syncthreads();
+                });
     } else if constexpr (CHN) {
         // per token block, the row scale of this lane's row, then per weight
         // block the four channels' scales and biases, read from the copies in

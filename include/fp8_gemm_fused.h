@@ -54,8 +54,11 @@ typedef enum {
  *     pointer NULL = 1.
  *   bias: [N] floats or NULL = 0.  Scales and bias 4-byte aligned.
  *   R: [M][ldr] BF16 or NULL = 0.  R may be D itself, with ldr = ldd.
- * M <= 64 takes the swapped decode kernel (4 waves splitting K over 16 or 32
- * weight rows), larger M the LDS-tiled one.
+ * The kernel is chosen by an estimate of its time (fp8_gemm_fused_plan): for
+ * few tokens or few output columns the swapped decode kernel (4 waves
+ * splitting K over 16 or 32 weight rows, tokens in tiles of up to 64), else
+ * the LDS-tiled one with 128 x 128, 128 x 256 or 256 x 256 tiles.  The choice
+ * never changes which elements are written.
  */
 int fp8_gemm_nt_fused(const void *A, int64_t lda, int a_dtype, const void *B, int64_t ldb, int b_dtype,
                       const float *scale_a, int scale_a_n, const float *scale_b, int scale_b_n,
@@ -128,6 +131,18 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
 
 /* Bytes of workspace of the call above (a negative fp8g_status for bad sizes). */
 int64_t bf16_gated_nt_backward_workspace(int M, int N);
+
+/*
+ * Kernel choice for a problem, without launching anything (host only).
+ *   op: 0 = fp8_gemm_nt_fused, 1 = fp8_gated_nt, 2 = bf16_gemm_nt_fused,
+ *   3 = bf16_gated_nt, 4 = one BF16 backward product (m x n outputs, reduced
+ *   over k; the gated weight gradients are one of 2 N x K).
+ * Fills the plan of fp8_gemm.h: variant 1 = tiled 256 x 256, 2 = tiled 128 x
+ * 256, 7 = tiled 128 x 128 (m x n of the products; the gated forms' tiles hold
+ * half as many output columns), 4 = swapped decode, 0 = nothing to launch;
+ * tile_m and tile_n in rows and columns of D.
+ */
+int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out);
 
 #ifdef __cplusplus
 }

@@ -163,3 +163,60 @@ def test_gated_bf16_backward(f, M, N, K, name):
     F.check(ga, *(x + y for x, y in zip(p, q)), N, f"grad_a {name}")
     F.check(gg, *F.backward_products(dp.t(), err_p.t(), a), M, f"grad_gate {name}")
     F.check(gu, *F.backward_products(du.t(), err_u.t(), a), M, f"grad_up {name}")
+
+
+# Every class of the tiled kernels with ragged edges, by the plan: (op, M, N, K) with few K so that the 64-bit
+# reference stays small.
+CLASS_CASES = [(0, 4000, 3000, 144, 1), (0, 2000, 2050, 272, 2), (0, 700, 1300, 272, 7), (0, 300, 70, 272, 4),
+               (1, 3000, 2100, 144, 1), (1, 2000, 1025, 272, 2), (1, 500, 1300, 272, 7), (1, 200, 70, 272, 4),
+               (2, 4000, 3000, 136, 1), (2, 2000, 2050, 200, 2), (2, 700, 1300, 200, 7), (2, 300, 70, 200, 4),
+               (3, 3000, 2100, 136, 1), (3, 2000, 1025, 200, 2), (3, 500, 1300, 200, 7), (3, 200, 70, 200, 4)]
+
+
+@pytest.mark.parametrize("op,M,N,K,variant", CLASS_CASES)
+def test_every_class(f, op, M, N, K, variant):
+    assert f.fused_plan(op, M, N, K).variant == variant
+    dt = E4 if op < 2 else BF
+    a, b = rand(1, M, K, dtype=dt), rand(2, N, K, dtype=dt, std=0.25)
+    if op in (0, 2):
+        bias, res = rand(3, N, dtype=torch.float32), rand(4, M, N)
+        call = f.gemm_nt_fused if op == 0 else f.gemm_nt_bf16_fused
+        out = call(a, b, bias=bias, activation="gelu", residual=res)
+        _, v, tight, hw = F.fused_reference(a, b, bias=bias, name="gelu", res=res)
+    else:
+        u = rand(5, N, K, dtype=dt, std=0.25)
+        out = (f.gated_nt if op == 1 else f.gated_nt_bf16)(a, b, u, activation="silu")
+        _, _, v, tight, hw = F.gated_reference(a, b, u)
+    F.check(out, v, tight, hw, K, f"op {op}")
+
+
+@pytest.mark.parametrize("M,N,K,va,vb", [(4000, 72, 3000, 1, 7), (2000, 205, 2056, 2, 7), (72, 4000, 3000, 7, 1),
+                                         (200, 2000, 2056, 7, 2), (300, 400, 520, 7, 7)])
+def test_every_backward_class(f, M, N, K, va, vb):
+    """grad_a is M x K reduced over N, grad_b N x K reduced over M."""
+    cols = (N + 63) // 64 * 64
+    assert f.fused_plan(4, M, K, cols).variant == va and f.fused_plan(4, N, K, M).variant == vb
+    a, b, G = rand(1, M, K), rand(2, N, K, std=0.25), rand(3, M, N)
+    z = rand(4, M, N, dtype=torch.float32)
+    ga, gb, _ = f.gemm_nt_bf16_fused_backward(G, a, b, activation="silu", preact=z)
+    g64, z64 = G.cpu().double(), z.cpu().double()
+    dz = g64 * F.act("silu", z64)[1]
+    err = grad_error("silu", g64, z64, torch.zeros_like(z64))
+    F.check(ga, *F.backward_products(dz, err, b), N, "grad_a")
+    F.check(gb, *F.backward_products(dz.t(), err.t(), a), M, "grad_b")
+
+
+@pytest.mark.parametrize("M,N,K,va,vw", [(4000, 36, 3000, 1, 7), (72, 2000, 3000, 7, 1)])
+def test_every_gated_backward_class(f, M, N, K, va, vw):
+    cols = (N + 63) // 64 * 64
+    assert f.fused_plan(4, M, K, 2 * cols).variant == va and f.fused_plan(4, 2 * N, K, M).variant == vw
+    a, wg, wu, G = rand(1, M, K), rand(2, N, K, std=0.25), rand(5, N, K, std=0.25), rand(3, M, N)
+    pre = rand(4, 2 * M, N, dtype=torch.float32).view(2, M, N)
+    ga, gg, gu = f.gated_nt_bf16_backward(G, a, wg, wu, pre)
+    g64, (g, u) = G.cpu().double(), pre.cpu().double()
+    v, dv = F.act("silu", g)
+    dp, du = g64 * u * dv, g64 * v
+    ep, eu = grad_error("silu", g64 * u, g, torch.zeros_like(g)), g64.abs() * 2.0 ** -19 * g.abs()
+    F.check(ga, *(x + y for x, y in zip(F.backward_products(dp, ep, wg), F.backward_products(du, eu, wu))), N, "grad_a")
+    F.check(gg, *F.backward_products(dp.t(), ep.t(), a), M, "grad_gate")
+    F.check(gu, *F.backward_products(du.t(), eu.t(), a), M, "grad_up")
