@@ -454,91 +454,123 @@ def _activation(name):
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
 
 
-def _call(device, fn, *args):
-    """fn(*args, stream) on the current stream of `device`."""
-    torch = _torch()
-    index = device.index
-    if index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
-        return
-    with torch.cuda.device(index):
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+# What the wrappers below look up on every call, once: a few-token kernel takes less time than the
+# argument checks did through `import torch`, torch.device objects and torch.cuda.Stream.
+class _Torch:
+    def __init__(self):
+        import torch
+        self.bf16, self.f32, self.empty = torch.bfloat16, torch.float32, torch.empty
+        self.fp8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+        self.current_device, self.guard = torch.cuda.current_device, torch.cuda.device
+        # the current stream's handle without a Stream object around it, where torch offers that
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _same_device(device, **tensors):
-    if device.type != "cuda":
+_cached = None
+
+
+def _tt():
+    global _cached
+    if _cached is None:
+        _cached = _Torch()
+    return _cached
+
+
+def _call(tt, index, fn, *args):
+    """fn(*args, stream) on the current stream of device `index`."""
+    if index == tt.current_device():
+        status = fn(*args, tt.stream(index))
+    else:
+        with tt.guard(index):
+            status = fn(*args, tt.stream(index))
+    if status:
+        _check(status)
+
+
+def _device(a, *others):
+    """The GPU of `a`, which the other tensors (or None) must share."""
+    index = a.get_device()
+    if index < 0:
         raise ValueError("all tensors must be on the GPU")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, a on {device}")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on one GPU: {t.device} and {a.device}")
+    return index
 
 
-def _rows(t, name, shape, dtype):
-    """Check a matrix with unit column stride and rows that do not overlap; its row stride."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a {list(shape)} {dtype} tensor, got {list(t.shape)} {t.dtype}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    if rows <= 1 or cols == 0:
-        return cols
-    if t.stride(0) < cols:
-        raise ValueError(f"{name}: row stride {t.stride(0)} below {cols}")
-    return t.stride(0)
+def _matrices(a, b, bname):
+    """M, N, K of a [M, K] and b [N, K]."""
+    sa, sb = a.shape, b.shape
+    if len(sa) != 2 or len(sb) != 2 or sa[1] != sb[1]:
+        raise ValueError(f"shapes {tuple(sa)} and {tuple(sb)} of a and {bname} are not [M, K] and [N, K]")
+    return sa[0], sb[0], sa[1]
 
 
-def _operand(t, name, K, grain):
-    """Check a K-contiguous operand; its row stride in elements (one that satisfies the library
-    where torch's is arbitrary: a single row or an empty matrix)."""
-    if t.dim() != 2 or t.shape[1] != K:
-        raise ValueError(f"{name} must be a [*, {K}] matrix, got {list(t.shape)}")
-    if K > 1 and t.stride(1) != 1:
+def _fp8_of(tt, t, dtype_arg, name):
+    code = tt.fp8.get(t.dtype)
+    if code is None or (dtype_arg is not None and dtype_arg != code):
+        return _fp8_code(t, dtype_arg, name)
+    return code
+
+
+def _operand(t, name, rows, K, grain):
+    """The row stride in elements of a K-contiguous [rows, K] operand (one that satisfies the library where
+    torch's is arbitrary: a single row or an empty matrix)."""
+    ld, unit = t.stride()
+    if unit != 1 and K > 1:
         raise ValueError(f"{name} must be K-contiguous (stride(1) == 1)")
-    if t.shape[0] <= 1 or K == 0:
-        return (K + grain - 1) // grain * grain
-    return t.stride(0)
+    return ld if rows > 1 and K else (K + grain - 1) // grain * grain
 
 
-def _output(out, name, M, N, device):
-    """The BF16 output and its row stride: allocated with rows padded to 8 elements if not given."""
-    torch = _torch()
+def _rows(t, name, M, N, dtype):
+    """The row stride of a [M, N] matrix with unit column stride whose rows do not overlap."""
+    if t.dtype != dtype or t.dim() != 2 or tuple(t.shape) != (M, N):
+        raise ValueError(f"{name} must be a [{M}, {N}] {dtype} tensor, got {list(t.shape)} {t.dtype}")
+    ld, unit = t.stride()
+    if unit != 1 and N > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if M <= 1 or N == 0:
+        return N
+    if ld < N:
+        raise ValueError(f"{name}: row stride {ld} below {N}")
+    return ld
+
+
+def _new(tt, M, N, device):
+    """A BF16 [M, N] output in rows padded to 8 elements, and its row stride."""
+    ld = (N + 7) // 8 * 8
+    out = tt.empty((M, ld), dtype=tt.bf16, device=device)
+    return (out if ld == N else out[:, :N]), ld
+
+
+def _output(tt, out, a, index, M, N):
     if out is None:
-        ld = (N + 7) // 8 * 8
-        out = torch.empty((M, ld), dtype=torch.bfloat16, device=device)
-        return (out if ld == N else out[:, :N]), max(ld, 8)
-    ld = _rows(out, name, (M, N), torch.bfloat16)
-    if out.device != device:
-        raise ValueError(f"{name} is on {out.device}, a on {device}")
+        return _new(tt, M, N, a.device)
+    if out.get_device() != index:
+        raise ValueError(f"out is on {out.device}, a on {a.device}")
+    ld = _rows(out, "out", M, N, tt.bf16)
     return out, (ld if M > 1 else (N + 7) // 8 * 8)
 
 
-def _floats(t, name, *sizes):
-    """A contiguous float32 vector of one of `sizes` values: (pointer, values)."""
+def _floats(tt, t, name, n, one=True):
+    """A contiguous float32 vector of n values (or, if `one`, of a single one): (pointer, values)."""
     if t is None:
         return None, 0
-    if t.dtype != _torch().float32 or t.numel() not in sizes or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor with {' or '.join(map(str, sizes))} element(s)")
-    return t.data_ptr(), t.numel()
+    count = t.numel()
+    if t.dtype != tt.f32 or not (count == n or (one and count == 1)) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor with {n}{' or 1' if one else ''} element(s)")
+    return t.data_ptr(), count
 
 
-def _residual(t, M, N):
-    if t is None:
-        return None, 0
-    ld = _rows(t, "residual", (M, N), _torch().bfloat16)
-    return t.data_ptr(), ld
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _bf16(*named):
-    torch = _torch()
-    for name, t in named:
-        if t.dtype != torch.bfloat16:
+def _bf16_only(tt, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != tt.bf16:
             raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-
-
-def _fused_shapes(a, b, bname="b"):
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
-        raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)} of a and {bname} are not [M, K] and [N, K]")
-    return a.shape[0], b.shape[0], a.shape[1]
 
 
 def gemm_nt_fused(a, b, scale_a=None, scale_b=None, bias=None, activation="none", residual=None, out=None,
@@ -552,18 +584,19 @@ def gemm_nt_fused(a, b, scale_a=None, scale_b=None, bias=None, activation="none"
     "silu", "gelu" (erf) or "gelu_tanh"; residual: bfloat16 [M, N] with any row
     stride, or None; it may be `out` itself.
     """
-    fa, fb = _fp8_code(a, a_dtype, "a"), _fp8_code(b, b_dtype, "b")
-    M, N, K = _fused_shapes(a, b)
-    dev = a.device
-    _same_device(dev, b=b, scale_a=scale_a, scale_b=scale_b, bias=bias, residual=residual)
-    lda, ldb = _operand(a, "a", K, 16), _operand(b, "b", K, 16)
-    sa, na = _floats(scale_a, "scale_a", M, 1)
-    sb, nb = _floats(scale_b, "scale_b", N, 1)
-    bp, _ = _floats(bias, "bias", N)
-    rp, ldr = _residual(residual, M, N)
-    out, ldd = _output(out, "out", M, N, dev)
-    _call(dev, load_library().fp8_gemm_nt_fused, a.data_ptr(), lda, fa, b.data_ptr(), ldb, fb, sa, na, sb, nb, bp,
-          _activation(activation), rp, ldr, out.data_ptr(), ldd, M, N, K)
+    tt = _tt()
+    fa, fb = _fp8_of(tt, a, a_dtype, "a"), _fp8_of(tt, b, b_dtype, "b")
+    M, N, K = _matrices(a, b, "b")
+    index = _device(a, b, scale_a, scale_b, bias, residual)
+    lda, ldb = _operand(a, "a", M, K, 16), _operand(b, "b", N, K, 16)
+    sa, na = _floats(tt, scale_a, "scale_a", M)
+    sb, nb = _floats(tt, scale_b, "scale_b", N)
+    bp, _ = _floats(tt, bias, "bias", N, one=False)
+    ldr = 0 if residual is None else _rows(residual, "residual", M, N, tt.bf16)
+    act = _activation(activation)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().fp8_gemm_nt_fused, a.data_ptr(), lda, fa, b.data_ptr(), ldb, fb, sa, na, sb, nb,
+          bp, act, _ptr(residual), ldr, out.data_ptr(), ldd, M, N, K)
     return out
 
 
@@ -575,26 +608,26 @@ def gemm_nt_bf16_fused(a, b, bias=None, activation="none", residual=None, out=No
     Arguments as for gemm_nt_fused.  preact: a float32 [M, N] tensor that
     receives z, for gemm_nt_bf16_fused_backward, or None.
     """
-    torch = _torch()
-    _bf16(("a", a), ("b", b))
-    M, N, K = _fused_shapes(a, b)
-    dev = a.device
-    _same_device(dev, b=b, bias=bias, residual=residual, preact=preact)
-    lda, ldb = _operand(a, "a", K, 8), _operand(b, "b", K, 8)
-    bp, _ = _floats(bias, "bias", N)
-    rp, ldr = _residual(residual, M, N)
-    pp, ldp = (None, 0) if preact is None else (preact.data_ptr(), _rows(preact, "preact", (M, N), torch.float32))
-    out, ldd = _output(out, "out", M, N, dev)
-    _call(dev, load_library().bf16_gemm_nt_fused, a.data_ptr(), lda, b.data_ptr(), ldb, bp, _activation(activation),
-          rp, ldr, out.data_ptr(), ldd, pp, ldp, M, N, K)
+    tt = _tt()
+    _bf16_only(tt, a=a, b=b)
+    M, N, K = _matrices(a, b, "b")
+    index = _device(a, b, bias, residual, preact)
+    lda, ldb = _operand(a, "a", M, K, 8), _operand(b, "b", N, K, 8)
+    bp, _ = _floats(tt, bias, "bias", N, one=False)
+    ldr = 0 if residual is None else _rows(residual, "residual", M, N, tt.bf16)
+    ldp = 0 if preact is None else _rows(preact, "preact", M, N, tt.f32)
+    act = _activation(activation)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().bf16_gemm_nt_fused, a.data_ptr(), lda, b.data_ptr(), ldb, bp, act, _ptr(residual),
+          ldr, out.data_ptr(), ldd, _ptr(preact), ldp, M, N, K)
     return out
 
 
-def _workspace(size, device):
-    torch = _torch()
+def _workspace(tt, size, device):
     if size < 0:
         _check(size)
-    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    import torch
+    return tt.empty(size, dtype=torch.uint8, device=device) if size else None
 
 
 def gemm_nt_bf16_fused_backward(grad_out, a, b, activation="none", preact=None, bias_grad=False, a_grad=True,
@@ -608,29 +641,31 @@ def gemm_nt_bf16_fused_backward(grad_out, a, b, activation="none", preact=None, 
     "none").  grad_bias is float32 [N]; what a_grad, b_grad or bias_grad
     excludes is None.  The residual's gradient is grad_out itself.
     """
-    torch = _torch()
-    _bf16(("grad_out", grad_out), ("a", a), ("b", b))
-    M, N, K = _fused_shapes(a, b)
-    dev = a.device
-    _same_device(dev, b=b, grad_out=grad_out, preact=preact)
+    tt = _tt()
+    _bf16_only(tt, grad_out=grad_out, a=a, b=b)
+    M, N, K = _matrices(a, b, "b")
+    index = _device(a, b, grad_out, preact)
     act = _activation(activation)
-    lda, ldb = _operand(a, "a", K, 8), _operand(b, "b", K, 8)
-    ldg = _rows(grad_out, "grad_out", (M, N), torch.bfloat16)
+    lda, ldb = _operand(a, "a", M, K, 8), _operand(b, "b", N, K, 8)
+    ldg = _rows(grad_out, "grad_out", M, N, tt.bf16)
     if preact is None and act:
         raise ValueError(f"activation {activation!r} needs preact")
-    pp, ldp = (None, 0) if preact is None else (preact.data_ptr(), _rows(preact, "preact", (M, N), torch.float32))
-    ga, ldga = _output(None, "grad_a", M, K, dev) if a_grad else (None, 0)
-    gb, ldgb = _output(None, "grad_b", N, K, dev) if b_grad else (None, 0)
-    gbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
+    ldp = 0 if preact is None else _rows(preact, "preact", M, N, tt.f32)
+    dev = a.device
+    ga, ldga = _new(tt, M, K, dev) if a_grad else (None, 0)
+    gb, ldgb = _new(tt, N, K, dev) if b_grad else (None, 0)
+    gbias = tt.empty(N, dtype=tt.f32, device=dev) if bias_grad else None
     lib = load_library()
-    ws = _workspace(lib.bf16_gemm_nt_fused_backward_workspace(M, N), dev)
-    _call(dev, lib.bf16_gemm_nt_fused_backward, grad_out.data_ptr(), ldg, a.data_ptr(), lda, b.data_ptr(), ldb, pp,
-          ldp, act, _ptr(ga), ldga, _ptr(gb), ldgb, _ptr(gbias), _ptr(ws), 0 if ws is None else ws.numel(), M, N, K)
+    ws = _workspace(tt, lib.bf16_gemm_nt_fused_backward_workspace(M, N), dev)
+    _call(tt, index, lib.bf16_gemm_nt_fused_backward, grad_out.data_ptr(), ldg, a.data_ptr(), lda, b.data_ptr(), ldb,
+          _ptr(preact), ldp, act, _ptr(ga), ldga, _ptr(gb), ldgb, _ptr(gbias), _ptr(ws),
+          0 if ws is None else ws.numel(), M, N, K)
     return ga, gb, gbias
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _same_shape(t, name, N, K):
+    if tuple(t.shape) != (N, K):
+        raise ValueError(f"{name} is {list(t.shape)}, w_gate {[N, K]}")
 
 
 def gated_nt(a, w_gate, w_up, scale_a=None, scale_gate=None, scale_up=None, activation="silu", out=None,
@@ -644,32 +679,34 @@ def gated_nt(a, w_gate, w_up, scale_a=None, scale_gate=None, scale_up=None, acti
     merged [2 N, K] weight); scales as for gemm_nt_fused, scale_gate and
     scale_up of the same length.
     """
-    fa, fw = _fp8_code(a, a_dtype, "a"), _fp8_code(w_gate, w_dtype, "w_gate")
-    if _fp8_code(w_up, w_dtype, "w_up") != fw:
+    tt = _tt()
+    fa, fw = _fp8_of(tt, a, a_dtype, "a"), _fp8_of(tt, w_gate, w_dtype, "w_gate")
+    if _fp8_of(tt, w_up, w_dtype, "w_up") != fw:
         raise TypeError("w_gate and w_up must have one FP8 dtype")
-    M, N, K = _fused_shapes(a, w_gate, "w_gate")
-    if tuple(w_up.shape) != (N, K):
-        raise ValueError(f"w_up is {list(w_up.shape)}, w_gate {[N, K]}")
-    dev = a.device
-    _same_device(dev, w_gate=w_gate, w_up=w_up, scale_a=scale_a, scale_gate=scale_gate, scale_up=scale_up)
-    lda, ldg, ldu = _operand(a, "a", K, 16), _operand(w_gate, "w_gate", K, 16), _operand(w_up, "w_up", K, 16)
-    sa, na = _floats(scale_a, "scale_a", M, 1)
-    sg, ng = _floats(scale_gate, "scale_gate", N, 1)
-    su, nu = _floats(scale_up, "scale_up", N, 1)
-    if sg is not None and su is not None and ng != nu:
+    M, N, K = _matrices(a, w_gate, "w_gate")
+    _same_shape(w_up, "w_up", N, K)
+    index = _device(a, w_gate, w_up, scale_a, scale_gate, scale_up)
+    lda, ldg, ldu = _operand(a, "a", M, K, 16), _operand(w_gate, "w_gate", N, K, 16), _operand(w_up, "w_up", N, K, 16)
+    sa, na = _floats(tt, scale_a, "scale_a", M)
+    sg, ng = _floats(tt, scale_gate, "scale_gate", N)
+    su, nu = _floats(tt, scale_up, "scale_up", N)
+    if ng and nu and ng != nu:
         raise ValueError("scale_gate and scale_up must have one length")
-    out, ldd = _output(out, "out", M, N, dev)
-    _call(dev, load_library().fp8_gated_nt, a.data_ptr(), lda, fa, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, fw,
-          sa, na, sg, su, max(ng, nu), _activation(activation), out.data_ptr(), ldd, M, N, K)
+    act = _activation(activation)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().fp8_gated_nt, a.data_ptr(), lda, fa, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
+          fw, sa, na, sg, su, max(ng, nu), act, out.data_ptr(), ldd, M, N, K)
     return out
 
 
-def _gated_preact(preact, M, N):
-    """(gate, up, row stride) of a float32 [2, M, N] tensor."""
+def _gated_preact(tt, preact, M, N):
+    """(gate, up, row stride) pointers of a float32 [2, M, N] tensor."""
     if preact.dim() != 3 or preact.shape[0] != 2:
         raise ValueError(f"preact must be a [2, {M}, {N}] tensor, got {list(preact.shape)}")
-    gate, up = preact[0], preact[1]
-    return gate, up, _rows(gate, "preact", (M, N), _torch().float32)
+    gate = preact[0]
+    ld = _rows(gate, "preact", M, N, tt.f32)
+    pointer = gate.data_ptr()
+    return pointer, pointer + 4 * preact.stride(0), ld
 
 
 def gated_nt_bf16(a, w_gate, w_up, activation="silu", out=None, preact=None):
@@ -680,17 +717,17 @@ def gated_nt_bf16(a, w_gate, w_up, activation="silu", out=None, preact=None):
     preact: a float32 [2, M, N] tensor that receives g and u, for
     gated_nt_bf16_backward, or None.
     """
-    _bf16(("a", a), ("w_gate", w_gate), ("w_up", w_up))
-    M, N, K = _fused_shapes(a, w_gate, "w_gate")
-    if tuple(w_up.shape) != (N, K):
-        raise ValueError(f"w_up is {list(w_up.shape)}, w_gate {[N, K]}")
-    dev = a.device
-    _same_device(dev, w_gate=w_gate, w_up=w_up, preact=preact)
-    lda, ldg, ldu = _operand(a, "a", K, 8), _operand(w_gate, "w_gate", K, 8), _operand(w_up, "w_up", K, 8)
-    pg, pu, ldp = (None, None, 0) if preact is None else _gated_preact(preact, M, N)
-    out, ldd = _output(out, "out", M, N, dev)
-    _call(dev, load_library().bf16_gated_nt, a.data_ptr(), lda, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
-          _activation(activation), out.data_ptr(), ldd, _ptr(pg), _ptr(pu), ldp, M, N, K)
+    tt = _tt()
+    _bf16_only(tt, a=a, w_gate=w_gate, w_up=w_up)
+    M, N, K = _matrices(a, w_gate, "w_gate")
+    _same_shape(w_up, "w_up", N, K)
+    index = _device(a, w_gate, w_up, preact)
+    lda, ldg, ldu = _operand(a, "a", M, K, 8), _operand(w_gate, "w_gate", N, K, 8), _operand(w_up, "w_up", N, K, 8)
+    pg, pu, ldp = (None, None, 0) if preact is None else _gated_preact(tt, preact, M, N)
+    act = _activation(activation)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().bf16_gated_nt, a.data_ptr(), lda, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu,
+          act, out.data_ptr(), ldd, pg, pu, ldp, M, N, K)
     return out
 
 
@@ -701,25 +738,25 @@ def gated_nt_bf16_backward(grad_out, a, w_gate, w_up, preact, activation="silu",
         dg = grad_out * u * act'(g);  du = grad_out * act(g)
         grad_a = bf16(dg . w_gate + du . w_up);  grad_gate = bf16(dg^T . a);  grad_up = bf16(du^T . a)
 
-    preact: the tensor that the forward call filled.  What a_grad or w_grad
-    excludes is None.
+    preact: the tensor that the forward call filled.  w_gate and w_up share one
+    row stride.  What a_grad or w_grad excludes is None.
     """
-    torch = _torch()
-    _bf16(("grad_out", grad_out), ("a", a), ("w_gate", w_gate), ("w_up", w_up))
-    M, N, K = _fused_shapes(a, w_gate, "w_gate")
-    if tuple(w_up.shape) != (N, K):
-        raise ValueError(f"w_up is {list(w_up.shape)}, w_gate {[N, K]}")
+    tt = _tt()
+    _bf16_only(tt, grad_out=grad_out, a=a, w_gate=w_gate, w_up=w_up)
+    M, N, K = _matrices(a, w_gate, "w_gate")
+    _same_shape(w_up, "w_up", N, K)
+    index = _device(a, w_gate, w_up, grad_out, preact)
+    lda, ldg, ldu = _operand(a, "a", M, K, 8), _operand(w_gate, "w_gate", N, K, 8), _operand(w_up, "w_up", N, K, 8)
+    ldgrad = _rows(grad_out, "grad_out", M, N, tt.bf16)
+    pg, pu, ldp = _gated_preact(tt, preact, M, N)
+    act = _activation(activation)
     dev = a.device
-    _same_device(dev, w_gate=w_gate, w_up=w_up, grad_out=grad_out, preact=preact)
-    lda, ldg, ldu = _operand(a, "a", K, 8), _operand(w_gate, "w_gate", K, 8), _operand(w_up, "w_up", K, 8)
-    ldgrad = _rows(grad_out, "grad_out", (M, N), torch.bfloat16)
-    pg, pu, ldp = _gated_preact(preact, M, N)
-    ga, ldga = _output(None, "grad_a", M, K, dev) if a_grad else (None, 0)
-    gw, ldgw = _output(None, "grad_gate", N, K, dev) if w_grad else (None, 0)
-    gu = _output(None, "grad_up", N, K, dev)[0] if w_grad else None
+    ga, ldga = _new(tt, M, K, dev) if a_grad else (None, 0)
+    gw, ldgw = _new(tt, N, K, dev) if w_grad else (None, 0)
+    gu = _new(tt, N, K, dev)[0] if w_grad else None
     lib = load_library()
-    ws = _workspace(lib.bf16_gated_nt_backward_workspace(M, N), dev)
-    _call(dev, lib.bf16_gated_nt_backward, grad_out.data_ptr(), ldgrad, a.data_ptr(), lda, w_gate.data_ptr(), ldg,
-          w_up.data_ptr(), ldu, pg.data_ptr(), pu.data_ptr(), ldp, _activation(activation), _ptr(ga), ldga, _ptr(gw),
-          _ptr(gu), ldgw, _ptr(ws), 0 if ws is None else ws.numel(), M, N, K)
+    ws = _workspace(tt, lib.bf16_gated_nt_backward_workspace(M, N), dev)
+    _call(tt, index, lib.bf16_gated_nt_backward, grad_out.data_ptr(), ldgrad, a.data_ptr(), lda, w_gate.data_ptr(),
+          ldg, w_up.data_ptr(), ldu, pg, pu, ldp, act, _ptr(ga), ldga, _ptr(gw), _ptr(gu), ldgw, _ptr(ws),
+          0 if ws is None else ws.numel(), M, N, K)
     return ga, gw, gu

@@ -10,13 +10,13 @@ using fp8g::EPI_STORE;
 using fp8g::FMT_BF16;
 using fp8g::GradParams;
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool TA, bool TB, int EPI>
+template <int BM, int BN, int STAGES, bool TA, bool TB, int EPI>
 int launch_shape(const FusedArgs &a, int ny, hipStream_t s) {
     auto p = with_epilogue<EPI, false>(a);
     p.tiles_m = (int)cdiv(p.M, BM);
     p.tiles_n = (int)cdiv(p.N, EPI == EPI_GATED ? BN / 2 : BN);
-    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny), block(64 * WM * WN);
-    hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, WM, WN, STAGES, TA, TB, EPI>), grid, block, 0, s, p);
+    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny), block(256);
+    hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, STAGES, TA, TB, EPI>), grid, block, 0, s, p);
     return launch_status("fused BF16 tiled kernel");
 }
 
@@ -24,9 +24,9 @@ int launch_shape(const FusedArgs &a, int ny, hipStream_t s) {
 // (grid y).
 template <bool TA, bool TB, int EPI>
 int launch_tile(ShapeClass c, const FusedArgs &a, int ny, hipStream_t s) {
-    if (c == C_128x128) return launch_shape<128, 128, 2, 2, 4, TA, TB, EPI>(a, ny, s);
-    if (c == C_128x256) return launch_shape<128, 256, 2, 4, 3, TA, TB, EPI>(a, ny, s);
-    return launch_shape<256, 256, 4, 2, 2, TA, TB, EPI>(a, ny, s);
+    if (c == C_128x128) return launch_shape<128, 128, 4, TA, TB, EPI>(a, ny, s);
+    if (c == C_128x256) return launch_shape<128, 256, 3, TA, TB, EPI>(a, ny, s);
+    return launch_shape<256, 256, 2, TA, TB, EPI>(a, ny, s);
 }
 
 // The forward products.  The few-token kernel counts K and the operands'

@@ -3,51 +3,67 @@
 // pre-activations and of the bias.
 #pragma once
 
+#include <utility>
+
 #include "fused.hpp"
 
 namespace fp8g {
 
 // ---------------------------------------------------------------------------
-// BF16 tiled kernel.  BM x BN outputs per workgroup of WM x WN waves on
-// v_mfma 32x32x16, K in steps of 64 elements through a direct-to-LDS ring of
-// STAGES slots, as in ring_kernel: fragments read one K half ahead of the
-// matrix instructions, one barrier per step, the refill of a step's slot
-// spread over the second half's instructions.
+// BF16 tiled kernel.  BM x BN outputs per workgroup of 4 waves (2 x 2) on
+// v_mfma 16x16x32, K in steps of 64 elements through a direct-to-LDS ring of
+// STAGES slots: fragments read one K half (32 elements) ahead of the matrix
+// instructions, one barrier per step, the refill of a step's slot spread over
+// the second half's instructions.
 //
 // Either operand may be K-contiguous (rows of K elements: ring rows of 128
-// bytes, read with ds_read_b128) or K-strided (TA / TB: rows of the operand's
+// bytes, read with ds_read_b128; 16-byte chunk c of row r stored at c ^ ((r >>
+// 1) & 7), as in tile16_body) or K-strided (TA / TB: rows of the operand's
 // other dimension, one per K element: ring rows of BM or BN elements), so that
 // the backward products need no transposed copies of the weights, tokens or
 // gradients.  A K-strided fragment comes from ds_read_b64_tr_b16, which gives
 // lane i of each 16 lanes column i of a 4 x 16 block of 16-bit values: 4 K
-// elements of one row of the operand.  Four of them make the 32 bytes of a
+// elements of one row of the operand.  Two of them make the 16 bytes of a
 // lane's fragment, in the K order of the K-contiguous form.  The 32-byte
-// segments of a K-strided ring row k are stored at segment ^ 2 (k % 4): the 4
-// rows and 2 segments that half a wave reads then lie in different banks.
+// segments of a K-strided ring row k are stored at segment ^ strided_key(k):
+// the 4 rows that 16 lanes read, and the 8 rows of 32 lanes, lie in different
+// banks.
 //
-// Gated: blocks of 32 ring rows alternate between p.B and p.B2.
+// Gated: blocks of 16 ring rows alternate between p.B and p.B2.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ int strided_key(int k) { return 2 * (k & 3) + ((k >> 3) & 1); }
+
+// f(int_c<0>{}), ..., f(int_c<N - 1>{})
+template <class F, int... I>
+__device__ __forceinline__ void static_for_each(F f, std::integer_sequence<int, I...>) {
+    (f(int_c<I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+    static_for_each(f, std::make_integer_sequence<int, N>{});
+}
+
 typedef short v4s __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v2u lds_read_tr16(const uint8_t *a) {
     return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)a));
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool TA, bool TB, int EPI>
-__global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<EPI, false> p) {
+template <int BM, int BN, int STAGES, bool TA, bool TB, int EPI>
+__global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, false> p) {
     constexpr bool GATED = EPI == EPI_GATED;
     static_assert(!GATED || (!TA && !TB), "gated: K-contiguous operands");
     constexpr int BK = 128, KE = BK / 2;           // a K step: bytes, elements
-    constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
-    constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+    constexpr int WM = 2, WN = 2, WAVES = WM * WN, THREADS = 64 * WAVES;
+    constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
     constexpr int SLOT = (BM + BN) * BK;
     constexpr int CPA = BM / 8 / WAVES, CPB = BN / 8 / WAVES, CPW = CPA + CPB;   // 1 KB copies per wave per step
     constexpr int RING = STAGES * SLOT;
     constexpr int FPASS = (BM * BN * 4 + RING - 1) / RING, RW = TM / FPASS;   // epilogue passes, rows of a wave in each
-    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && CPA % 2 == 0 && CPB % 2 == 0, "copies split evenly");
-    static_assert(!GATED || (CPB == 4 && FN % 2 == 0), "gated: each wave copies rows of one matrix");
-    static_assert(STAGES >= 2 && RING <= 160 * 1024 && CPW * (STAGES - 1) < 64, "ring");
-    static_assert(RW % 32 == 0, "epilogue rows");
+    static_assert(CPA % 4 == 0 && CPB % 4 == 0, "copies split evenly");
+    static_assert(STAGES >= 2 && CPW * (STAGES - 1) < 64, "ring");
+    static_assert(FPASS <= 2 && RW % 16 == 0, "epilogue rows");
     constexpr int TERMS = EPI == EPI_ACT ? 3 * 1024 : 0;   // (copy_tile_terms; the biases are used)
+    static_assert(RING + TERMS <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + TERMS];
 
     const int tid = threadIdx.x;
@@ -67,21 +83,25 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
 
     // ---- copies ----
     // K-contiguous: copy qq fills ring rows 8 qq .. 8 qq + 7, lane l row l / 8,
-    // stored chunk l % 8 holding logical chunk (l % 8) ^ ring_key(row); the key
+    // stored chunk l % 8 holding logical chunk (l % 8) ^ key(row); the key
     // depends on qq through its parity only.  K-strided: copy qq fills 512 /
     // rows elements (2 or 4 K rows), lane l stored chunk l % (rows / 8) of row
     // l / (rows / 8).  A lane's offset within the tile is fixed per copy; each
     // step moves the descriptor's base and byte count.
+    auto key16 = [](uint32_t row) { return (row >> 1) & 7u; };
     const uint32_t lr = (uint32_t)lane / 8;
-    const uint32_t kc0 = (((uint32_t)lane % 8) ^ ring_key<128>(lr)) * 16u;
-    const uint32_t kc1 = (((uint32_t)lane % 8) ^ ring_key<128>(8 + lr)) * 16u;
+    const uint32_t kc0 = (((uint32_t)lane % 8) ^ key16(lr)) * 16u;
+    const uint32_t kc1 = (((uint32_t)lane % 8) ^ key16(8 + lr)) * 16u;
     auto strided_off = [&](int qq, int rows, int valid, int64_t ld) -> uint32_t {
         const int cpr = rows / 8;                  // 16-byte chunks per ring row
         const int k = qq * (512 / rows) + lane / cpr, pos = lane % cpr;
-        const int col = (((pos >> 1) ^ (2 * (k & 3))) * 16) + (pos & 1) * 8;
+        const int col = ((pos >> 1) ^ strided_key(k)) * 16 + (pos & 1) * 8;
         // (columns come in whole chunks: the caller's `valid` is rounded up to 8)
         return col < valid ? (uint32_t)k * (uint32_t)ld + 2u * (uint32_t)col : kOobOffset;
     };
+    // Gated: copies 4 q, 4 q + 1 fill ring rows 32 q .. + 15 with rows 16 q ..
+    // + 15 of p.B, 4 q + 2 and 4 q + 3 the next 16 with those of p.B2 (a second
+    // descriptor).
     uint32_t lo_a[CPA], lo_b[CPB];
 #pragma unroll
     for (int i = 0; i < CPA; ++i) {
@@ -89,34 +109,35 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
         lo_a[i] = TA ? strided_off(qq, BM, (rows_m + 7) & ~7, p.lda)
                      : (uint32_t)(qq * 8 + (int)lr) * (uint32_t)p.lda + ((i & 1) ? kc1 : kc0);
     }
-    const bool second = GATED && (wave & 1);       // this wave copies rows of p.B2
-    const int64_t ldb = second ? p.ldb2 : p.ldb;
 #pragma unroll
     for (int i = 0; i < CPB; ++i) {
         const int qq = wave * CPB + i;
-        const int row = GATED ? (qq / 8) * 32 + (qq % 4) * 8 + (int)lr : qq * 8 + (int)lr;
+        const int row = GATED ? (qq / 4) * 16 + (qq & 1) * 8 + (int)lr : qq * 8 + (int)lr;
         lo_b[i] = TB ? strided_off(qq, BN, (rows_n + 7) & ~7, p.ldb)
-                     : (uint32_t)row * (uint32_t)ldb + ((i & 1) ? kc1 : kc0);
+                     : (uint32_t)row * (uint32_t)(GATED && (i & 2) ? p.ldb2 : p.ldb) + ((i & 1) ? kc1 : kc0);
     }
     const uint8_t *const a0 = p.A + (int64_t)y * p.a_gstride + (TA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
-    const uint8_t *const b0 = (second ? p.B2 : p.B) + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * ldb);
-    const uint8_t *const b1 = TB ? p.B2 + (int64_t)n0 * 2 : b0;   // rows of K steps from ksplit on
-    const uint32_t bytes_a = rows_bytes(rows_m, p.lda), bytes_b = rows_bytes(rows_n, ldb);
-    v4i srdA, srdB;
+    const uint8_t *const b0 = p.B + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
+    // K-strided: rows of K steps from ksplit on; gated: the second matrix
+    const uint8_t *const b1 = p.B2 + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb2);
+    const uint32_t bytes_a = rows_bytes(rows_m, p.lda), bytes_b = rows_bytes(rows_n, p.ldb);
+    const uint32_t bytes_b1 = rows_bytes(rows_n, p.ldb2);
+    v4i srdA, srdB, srdB1 = {0, 0, 0, 0};
     uint32_t lds_a = 0, lds_b = 0, ko0 = 0, ko1 = 0;
     auto set_step = [&](int kd) {
-        if (TA) {
+        if constexpr (TA) {
             srdA = make_srd(a0 + (int64_t)kd * KE * p.lda, rows_bytes(min(KE, p.K - kd * KE), p.lda));
         } else {
             srdA = make_srd(a0 + (int64_t)kd * BK, kd < nk ? bytes_a - (uint32_t)(kd * BK) : 0u);
         }
-        if (TB) {
+        if constexpr (TB) {
             const bool late = kd >= p.ksplit;
             const int ks = late ? kd - p.ksplit : kd;
             srdB = make_srd((late ? b1 : b0) + (int64_t)ks * KE * p.ldb,
                             kd < nk ? rows_bytes(min(KE, p.krows - ks * KE), p.ldb) : 0u);
         } else {
             srdB = make_srd(b0 + (int64_t)kd * BK, kd < nk ? bytes_b - (uint32_t)(kd * BK) : 0u);
+            if constexpr (GATED) srdB1 = make_srd(b1 + (int64_t)kd * BK, kd < nk ? bytes_b1 - (uint32_t)(kd * BK) : 0u);
         }
         lds_a = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)(wave * CPA) * 1024u;
         lds_b = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)BM * BK + (uint32_t)(wave * CPB) * 1024u;
@@ -126,64 +147,59 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
         ko1 = (int)kc1 < lim ? 0u : kOobOffset;
     };
     auto issue_one = [&](int i) {
-        const uint32_t ko = (i & 1) ? ko1 : ko0;
-        if (i < CPA) dma16_m0(srdA, TA ? lo_a[i < CPA ? i : 0] : lo_a[i < CPA ? i : 0] + ko, lds_a + (uint32_t)i * 1024u);
-        else dma16_m0(srdB, TB ? lo_b[i < CPA ? 0 : i - CPA] : lo_b[i < CPA ? 0 : i - CPA] + ko,
+        const uint32_t ko = (i & 1) ? ko1 : ko0;   // (CPA is even)
+        if (i < CPA) dma16_m0(srdA, TA ? lo_a[i] : lo_a[i] + ko, lds_a + (uint32_t)i * 1024u);
+        else dma16_m0(GATED && ((i - CPA) & 2) ? srdB1 : srdB, TB ? lo_b[i - CPA] : lo_b[i - CPA] + ko,
                       lds_b + (uint32_t)(i - CPA) * 1024u);
     };
 
-    // ---- fragments: lane l carries row l % 32 of a 32-row block and, of each
-    // 32-element K half h, elements 16 (l / 32) .. + 15, in two parts of 8
-    const int lrow = lane & 31, khalf = lane >> 5;
-    const uint32_t key = ring_key<128>((uint32_t)lrow);
-    uint32_t fo[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            fo[h][j] = (uint32_t)lrow * BK + (((uint32_t)(4 * h + 2 * khalf + j) ^ key) & 7u) * 16u;
-    // K-strided: offset of block f (segments 2 f and 2 f + 1 of the wave's part)
-    const int trow = 16 * khalf + ((lane & 15) >> 2);
+    // ---- fragments: lane l carries row l % 16 of a 16-row block and, of K
+    // half h, elements 8 (l / 16) .. + 7
+    const int r16 = lane & 15, kg = lane >> 4;
+    const uint32_t key = key16((uint32_t)r16);
+    const uint32_t fo0 = (uint32_t)r16 * BK + (((uint32_t)kg ^ key) & 7u) * 16u;
+    const uint32_t fo1 = (uint32_t)r16 * BK + (((uint32_t)(4 + kg) ^ key) & 7u) * 16u;
+    // K-strided: offset of segment f of the wave's part
+    const int trow = 8 * kg + (r16 >> 2);
     uint32_t to_a[FM], to_b[FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f)
-        to_a[f] = (uint32_t)(trow * BM * 2 + (((wm * TM / 16 + 2 * f + ((lane >> 4) & 1)) ^ (2 * (trow & 3))) * 32) + (lane & 3) * 8);
+        to_a[f] = (uint32_t)(trow * BM * 2 + ((wm * FM + f) ^ strided_key(trow)) * 32 + (lane & 3) * 8);
 #pragma unroll
     for (int f = 0; f < FN; ++f)
-        to_b[f] = (uint32_t)(trow * BN * 2 + (((wn * TN / 16 + 2 * f + ((lane >> 4) & 1)) ^ (2 * (trow & 3))) * 32) + (lane & 3) * 8);
-    auto frag = [&](const uint8_t *base, bool strided, uint32_t to, int rowb, int h) -> v8i {
-        if (strided) {
+        to_b[f] = (uint32_t)(trow * BN * 2 + ((wn * FN + f) ^ strided_key(trow)) * 32 + (lane & 3) * 8);
+    auto frag = [&](auto strided, const uint8_t *base, uint32_t to, int rowb, int h) -> v4u {
+        if constexpr (strided.value) {
             const uint8_t *r = base + to + 32 * h * rowb;
             const v2u p0 = lds_read_tr16(r), p1 = lds_read_tr16(r + 4 * rowb);
-            const v2u p2 = lds_read_tr16(r + 8 * rowb), p3 = lds_read_tr16(r + 12 * rowb);
-            return pack8((v4u){p0[0], p0[1], p1[0], p1[1]}, (v4u){p2[0], p2[1], p3[0], p3[1]});
+            return (v4u){p0[0], p0[1], p1[0], p1[1]};
+        } else {
+            return *reinterpret_cast<const v4u *>(base + (h ? fo1 : fo0));
         }
-        return pack8(*reinterpret_cast<const v4u *>(base + fo[h][0]), *reinterpret_cast<const v4u *>(base + fo[h][1]));
     };
     // fragment q of K half h: weight block q < FN, else token block q - FN
-    auto read_frag = [&](v8i (&bf)[FN], v8i (&af)[FM], const uint8_t *slot, int h, int q) {
-        if (q < FN) bf[q < FN ? q : 0] = frag(slot + BM * BK + (TB ? 0 : (wn * TN + q * 32) * BK), TB, to_b[q < FN ? q : 0], BN * 2, h);
-        else af[q < FN ? 0 : q - FN] = frag(slot + (TA ? 0 : (wm * TM + (q - FN) * 32) * BK), TA, to_a[q < FN ? 0 : q - FN], BM * 2, h);
+    auto read_frag = [&](v4u (&bf)[FN], v4u (&af)[FM], const uint8_t *slot, int h, int q) {
+        if (q < FN) bf[q] = frag(int_c<TB>{}, slot + BM * BK + (TB ? 0 : (wn * TN + q * 16) * BK), to_b[q], BN * 2, h);
+        else af[q - FN] = frag(int_c<TA>{}, slot + (TA ? 0 : (wm * TM + (q - FN) * 16) * BK), to_a[q - FN], BM * 2, h);
     };
 
-    v16f acc[FN][FM];
+    v4f acc[FN][FM];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = (v16f){0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        for (int j = 0; j < FM; ++j) acc[i][j] = (v4f){0, 0, 0, 0};
 
-    // One K half of matrix instructions (all blocks' first parts, then their
-    // second parts: no instruction follows one on its own accumulator), with
-    // the next half's fragment reads and, in the second half, the refill of
-    // the step's slot spread between them.
-    constexpr int NT = FN * FM, NMF = 2 * NT, NFR = FN + FM;
-    auto half_step = [&](const v8i (&bf)[FN], const v8i (&af)[FM], v8i (&nb)[FN], v8i (&na)[FM], const uint8_t *read_slot,
+    // One K half of matrix instructions, with the next half's fragment reads
+    // and, in the second half, the refill of the step's slot spread between
+    // them.  (Unrolled by the template: the loop pragma gave up on K-strided
+    // operands.)
+    constexpr int NMF = FN * FM, NFR = FN + FM;
+    auto half_step = [&](const v4u (&bf)[FN], const v4u (&af)[FM], v4u (&nb)[FN], v4u (&na)[FM], const uint8_t *read_slot,
                          int read_h, int refill) {
-#pragma unroll
-        for (int t = 0; t < NMF; ++t) {
-            const int i = (t % NT) / FM, j = (t % NT) % FM;
-            if (t < NT) acc[i][j] = mfma32x32x16_bf16_part<0>(bf[i], af[j], acc[i][j]);
-            else acc[i][j] = mfma32x32x16_bf16_part<1>(bf[i], af[j], acc[i][j]);
+        static_for<NMF>([&](auto tc) {
+            constexpr int t = tc.value, i = t / FM, j = t % FM;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, bf[i]),
+                                                                __builtin_bit_cast(v8bf, af[j]), acc[i][j], 0, 0, 0);
 #pragma unroll
             for (int q = (t * NFR) / NMF; q < ((t + 1) * NFR) / NMF; ++q) read_frag(nb, na, read_slot, read_h, q);
             if (refill >= 0) {
@@ -192,11 +208,11 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
                 for (int q = (t * CPW) / NMF; q < ((t + 1) * CPW) / NMF; ++q) issue_one(q);
             }
             __builtin_amdgcn_sched_barrier(0);
-        }
+        });
     };
 
     if constexpr (EPI == EPI_ACT) copy_tile_terms(p, smem + RING, lds0 + (uint32_t)RING, wave, lane, m0, rows_m, n0, rows_n);
-    v8i f0b[FN], f0a[FM], f1b[FN], f1a[FM];
+    v4u f0b[FN], f0a[FM], f1b[FN], f1a[FM];
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
         set_step(s);
@@ -219,24 +235,26 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_tile_kernel(FusedParams<
     vmcnt_wait<0>();                               // drain the copies past the last step
     __syncthreads();                               // every wave's have landed; the ring is free
 
-    // ---- epilogue: register r of a block holds weight row 8 (r / 4) +
-    // 4 (l / 32) + r % 4 and token l % 32
+    // (pinned to AGPRs at the loop's exit: without this the 128-row builds carry
+    // the sums in VGPRs around the loop and copy them to AGPRs and back in every
+    // step)
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+
+    // ---- epilogue: register r of a block holds weight row 4 (l / 16) + r and
+    // token l % 16
     auto stage = [&](auto pass) {
 #pragma unroll
-        for (int jj = 0; jj < RW / 32; ++jj)
+        for (int jj = 0; jj < RW / 16; ++jj)
 #pragma unroll
             for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const v16f &c = acc[i][pass.value * (RW / 32) + jj];
-                    stage_f32<BN>(smem, wm * RW + jj * 32 + lrow, wn * TN + i * 32 + b * 8 + khalf * 4,
-                                  (v4f){c[4 * b], c[4 * b + 1], c[4 * b + 2], c[4 * b + 3]});
-                }
+                stage_f32<BN>(smem, wm * RW + jj * 16 + r16, wn * TN + i * 16 + kg * 4, acc[i][pass.value * (RW / 16) + jj]);
     };
-    static_assert(FPASS <= 2, "two branches below");
 #pragma unroll 1
     for (int h = 0; h < FPASS; ++h)
-        fused_store_rows<BN, WM * RW, THREADS, 32>(
+        fused_store_rows<BN, WM * RW, THREADS, 16>(
             p, smem, smem + RING, tid, m0, rows_m, n0, d, [=](int s) { return (s / RW) * TM + h * RW + s % RW; },
             [&] {
                 if (h == 0) {
