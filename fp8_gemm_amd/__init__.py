@@ -85,7 +85,7 @@ def load_library(path: str = LIB_PATH):
     lib.bf16_gemm_nt_fused.restype = I
     lib.bf16_gemm_nt_fused_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, I, P, I64, P, I64, P, P, I64, I, I, I, P]
     lib.bf16_gemm_nt_fused_backward.restype = I
-    lib.bf16_gemm_nt_fused_backward_workspace.argtypes = [I, I]
+    lib.bf16_gemm_nt_fused_backward_workspace.argtypes = [I, I, I]
     lib.bf16_gemm_nt_fused_backward_workspace.restype = I64
     lib.fp8_gated_nt.argtypes = [P, I64, I, P, I64, P, I64, I, P, I, P, P, I, I, P, I64, I, I, I, P]
     lib.fp8_gated_nt.restype = I
@@ -94,7 +94,7 @@ def load_library(path: str = LIB_PATH):
     lib.bf16_gated_nt_backward.argtypes = [P, I64, P, I64, P, I64, P, I64, P, P, I64, I, P, I64, P, P, I64, P, I64,
                                            I, I, I, P]
     lib.bf16_gated_nt_backward.restype = I
-    lib.bf16_gated_nt_backward_workspace.argtypes = [I, I]
+    lib.bf16_gated_nt_backward_workspace.argtypes = [I, I, I]
     lib.bf16_gated_nt_backward_workspace.restype = I64
     lib.fp8_gemm_fused_plan.argtypes = [I, I, I, I, ctypes.POINTER(Plan)]
     lib.fp8_gemm_fused_plan.restype = I
@@ -656,7 +656,7 @@ def gemm_nt_bf16_fused_backward(grad_out, a, b, activation="none", preact=None, 
     gb, ldgb = _new(tt, N, K, dev) if b_grad else (None, 0)
     gbias = tt.empty(N, dtype=tt.f32, device=dev) if bias_grad else None
     lib = load_library()
-    ws = _workspace(tt, lib.bf16_gemm_nt_fused_backward_workspace(M, N), dev)
+    ws = _workspace(tt, lib.bf16_gemm_nt_fused_backward_workspace(M, N, K), dev)
     _call(tt, index, lib.bf16_gemm_nt_fused_backward, grad_out.data_ptr(), ldg, a.data_ptr(), lda, b.data_ptr(), ldb,
           _ptr(preact), ldp, act, _ptr(ga), ldga, _ptr(gb), ldgb, _ptr(gbias), _ptr(ws),
           0 if ws is None else ws.numel(), M, N, K)
@@ -755,7 +755,7 @@ def gated_nt_bf16_backward(grad_out, a, w_gate, w_up, preact, activation="silu",
     gw, ldgw = _new(tt, N, K, dev) if w_grad else (None, 0)
     gu = _new(tt, N, K, dev)[0] if w_grad else None
     lib = load_library()
-    ws = _workspace(tt, lib.bf16_gated_nt_backward_workspace(M, N), dev)
+    ws = _workspace(tt, lib.bf16_gated_nt_backward_workspace(M, N, K), dev)
     _call(tt, index, lib.bf16_gated_nt_backward, grad_out.data_ptr(), ldgrad, a.data_ptr(), lda, w_gate.data_ptr(),
           ldg, w_up.data_ptr(), ldu, pg, pu, ldp, act, _ptr(ga), ldga, _ptr(gw), _ptr(gu), ldgw, _ptr(ws),
           0 if ws is None else ws.numel(), M, N, K)

@@ -19,6 +19,9 @@
 
 namespace fp8g {
 
+// One split of a backward product: FP32 sums into the workspace.
+constexpr int EPI_PARTIAL = 3;
+
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
 struct FusedArgs : GemmParams {
@@ -38,7 +41,8 @@ struct FusedArgs : GemmParams {
     int r_vec, p_vec;          // rows of R / pre start 16-byte aligned
     // Backward products: the second output (grid y = 1, whose A operand starts
     // a_gstride bytes later), the K step where B2's rows begin and the rows of
-    // each of B and B2.
+    // each of B and B2.  Split over K (grid z, ksteps steps each): the sums of
+    // split z of product y go to ws [z][y][M][N].
     uint16_t *D2;
     int ksplit, krows;
 };
@@ -300,7 +304,16 @@ __device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem
         const v2u lo = pack_bf16x4(o[0], o[1], o[2], o[3]), hi = pack_bf16x4(o[4], o[5], o[6], o[7]);
         store_chunk<MODE_DENSE>(d + (int64_t)m * p.ldd + n, (v4u){lo[0], lo[1], hi[0], hi[1]}, nv);
     };
-    if constexpr (EPI == EPI_STORE) {
+    if constexpr (EPI == EPI_PARTIAL) {
+        float *const sums = p.ws + ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * p.M * p.N;
+#pragma unroll U
+        for (int i = 0; i < NIT; ++i) {
+            const int s = s0 + i * RPI, r = row_of(s);
+            float z[8];
+            read8(s, c0, z);
+            if (r < rows_m) store_f32_row<8>(sums + (int64_t)(m0 + r) * p.N + n, nv, true, z);
+        }
+    } else if constexpr (EPI == EPI_STORE) {
 #pragma unroll U
         for (int i = 0; i < NIT; ++i) {
             const int s = s0 + i * RPI, r = row_of(s);

@@ -6,45 +6,52 @@ namespace {
 
 using fp8g::EPI_ACT;
 using fp8g::EPI_GATED;
+using fp8g::EPI_PARTIAL;
 using fp8g::EPI_STORE;
 using fp8g::FMT_BF16;
 using fp8g::GradParams;
 
+// grid: y over products sharing the launch, z over splits of K.
 template <int BM, int BN, int STAGES, bool TA, bool TB, int EPI>
-int launch_shape(const FusedArgs &a, int ny, hipStream_t s) {
+int launch_shape(const FusedArgs &a, int ny, int splits, hipStream_t s) {
     auto p = with_epilogue<EPI, false>(a);
     p.tiles_m = (int)cdiv(p.M, BM);
     p.tiles_n = (int)cdiv(p.N, EPI == EPI_GATED ? BN / 2 : BN);
-    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny), block(256);
+    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny, (unsigned)splits), block(256);
     hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, STAGES, TA, TB, EPI>), grid, block, 0, s, p);
     return launch_status("fused BF16 tiled kernel");
 }
 
-// The tiled kernel in the shape class `c`; ny: products sharing one launch
-// (grid y).
 template <bool TA, bool TB, int EPI>
-int launch_tile(ShapeClass c, const FusedArgs &a, int ny, hipStream_t s) {
-    if (c == C_128x128) return launch_shape<128, 128, 4, TA, TB, EPI>(a, ny, s);
-    if (c == C_128x256) return launch_shape<128, 256, 3, TA, TB, EPI>(a, ny, s);
-    return launch_shape<256, 256, 2, TA, TB, EPI>(a, ny, s);
+int launch_tile(ShapeClass c, const FusedArgs &a, int ny, int splits, hipStream_t s) {
+    if (c == C_128x128) return launch_shape<128, 128, 4, TA, TB, EPI>(a, ny, splits, s);
+    if (c == C_128x256) return launch_shape<128, 256, 3, TA, TB, EPI>(a, ny, splits, s);
+    return launch_shape<256, 256, 2, TA, TB, EPI>(a, ny, splits, s);
 }
 
 // The forward products.  The few-token kernel counts K and the operands'
 // strides in bytes, the tiled kernel K in elements.
 template <int EPI>
 int launch_forward(FusedArgs p, hipStream_t s) {
-    const ShapeClass c = pick_class(p.M, p.N, p.K, 2, EPI == EPI_GATED, true);
+    const ShapeClass c = pick_class(p.M, p.N, p.K, 2, EPI == EPI_GATED);
     if (c == C_FEW) {
         p.K *= 2;
         return launch_few_fmt<FMT_BF16, FMT_BF16, EPI>(p, s);
     }
-    return launch_tile<false, false, EPI>(c, p, 1, s);
+    return launch_tile<false, false, EPI>(c, p, 1, 1, s);
 }
 
-// A backward product.
+// A backward product (ny of them), its split sums in `sums`.
 template <bool TA, bool TB>
-int launch_backward(const FusedArgs &p, int ny, hipStream_t s) {
-    return launch_tile<TA, TB, EPI_STORE>(pick_class((int64_t)p.M * ny, p.N, p.K, 2, false, false), p, ny, s);
+int launch_backward(FusedArgs p, int ny, float *sums, hipStream_t s) {
+    const BackwardShape b = backward_shape(p.M, p.N, p.K, ny);
+    if (b.splits == 1) return launch_tile<TA, TB, EPI_STORE>(b.c, p, ny, 1, s);
+    p.ws = sums;
+    p.ksteps = b.ksteps;
+    if (const int st = launch_tile<TA, TB, EPI_PARTIAL>(b.c, p, ny, b.splits, s)) return st;
+    const dim3 grid((unsigned)cdiv((int64_t)p.M * p.N, 256 * 8), (unsigned)ny);
+    hipLaunchKernelGGL(fp8g::join_kernel, grid, dim3(256), 0, s, sums, b.splits, p.M, p.N, p.D, p.D2, p.ldd);
+    return launch_status("join kernel");
 }
 
 FusedArgs base_args(const void *A, int64_t lda, const void *B, int64_t ldb, void *D, int64_t ldd, int M, int N, int K) {
@@ -64,7 +71,17 @@ FusedArgs base_args(const void *A, int64_t lda, const void *B, int64_t ldb, void
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 int64_t pad256(int64_t n) { return (n + 255) / 256 * 256; }
 
+// Parts of the backward workspaces: the gradients of the pre-activations, the
+// bias gradient's partial sums, and the split sums of either product (dA [M x
+// K] reduced over `cols`, nw weight gradients [N x K] reduced over M), which
+// follow one another.
 int64_t grad_bytes(int64_t M, int64_t cols) { return pad256(2 * M * cols); }
+int64_t bias_bytes(int64_t M, int64_t N) { return pad256(4 * cdiv(M, fp8g::kGradRows) * N); }
+int64_t join_bytes(int64_t M, int64_t N, int64_t K, int64_t cols, int nw) {
+    if (K == 0) return 0;
+    const int64_t a = backward_shape(M, K, cols, 1).bytes, w = backward_shape(N, K, M, nw).bytes;
+    return a > w ? a : w;
+}
 
 int check_workspace(const void *ws, int64_t bytes, int64_t need) {
     if (need == 0) return FP8G_OK;
@@ -114,10 +131,10 @@ int bf16_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, c
     return launch_forward<EPI_ACT>(p, static_cast<hipStream_t>(stream));
 }
 
-int64_t bf16_gemm_nt_fused_backward_workspace(int M, int N) {
-    const int st = check_grad_sizes(M, N);
-    if (st) return st;
-    return grad_bytes(M, pad64(N)) + 4 * cdiv(M, fp8g::kGradRows) * N;
+int64_t bf16_gemm_nt_fused_backward_workspace(int M, int N, int K) {
+    int st;
+    if ((st = check_sizes(M, N, K, 2)) || (st = check_grad_sizes(M, N))) return st;
+    return grad_bytes(M, pad64(N)) + bias_bytes(M, N) + join_bytes(M, N, K, pad64(N), 1);
 }
 
 int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64_t lda, const void *B, int64_t ldb,
@@ -132,7 +149,7 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
         if ((st = check_rows("G", G, ldg, N, 2, &g_vec))) return st;
         if (activation != FP8G_ACT_NONE && !preact) return fail(FP8G_ERR_NULL, "preact is required");
         if (activation != FP8G_ACT_NONE && (st = check_rows("preact", preact, ldp, N, 4, &p_vec))) return st;
-        if ((st = check_workspace(workspace, workspace_bytes, bf16_gemm_nt_fused_backward_workspace(M, N)))) return st;
+        if ((st = check_workspace(workspace, workspace_bytes, bf16_gemm_nt_fused_backward_workspace(M, N, K)))) return st;
     }
     const bool want_a = dA && M > 0 && K > 0, want_b = dB && N > 0 && K > 0;
     if (want_a && ((N > 0 && (st = check_operand("B", B, ldb, K, 2))) || (st = check_output("dA", dA, ldda, K)))) return st;
@@ -146,6 +163,7 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
     const int64_t cols = pad64(N);
     uint16_t *const w = static_cast<uint16_t *>(workspace);
     float *const part = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, cols));
+    float *const sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, cols) + bias_bytes(M, N));
     if (M > 0 && N > 0 && (dbias || (!direct && (want_a || want_b)))) {
         GradParams g = {};
         g.G = static_cast<const uint16_t *>(G); g.ldg = ldg; g.g_vec = g_vec;
@@ -169,11 +187,11 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
         // workspace's dZ are zero, and B's rows past N read as zeros
         FusedArgs p = base_args(dz, ldz, B, ldb, dA, ldda, M, K, direct ? N : (int)cols);
         p.krows = N;
-        if ((st = launch_backward<false, true>(p, 1, s))) return st;
+        if ((st = launch_backward<false, true>(p, 1, sums, s))) return st;
     }
     if (want_b) {
         FusedArgs p = base_args(dz, ldz, A, lda, dB, lddb, N, K, M);
-        if ((st = launch_backward<true, true>(p, 1, s))) return st;
+        if ((st = launch_backward<true, true>(p, 1, sums, s))) return st;
     }
     return ok();
 }
@@ -198,10 +216,10 @@ int bf16_gated_nt(const void *A, int64_t lda, const void *Wg, int64_t ldg, const
     return launch_forward<EPI_GATED>(p, static_cast<hipStream_t>(stream));
 }
 
-int64_t bf16_gated_nt_backward_workspace(int M, int N) {
-    const int st = check_grad_sizes(M, N);
-    if (st) return st;
-    return grad_bytes(M, 2 * pad64(N));
+int64_t bf16_gated_nt_backward_workspace(int M, int N, int K) {
+    int st;
+    if ((st = check_sizes(M, N, K, 2)) || (st = check_grad_sizes(M, N))) return st;
+    return grad_bytes(M, 2 * pad64(N)) + join_bytes(M, N, K, 2 * pad64(N), 2);
 }
 
 int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t lda, const void *Wg, int64_t ldg,
@@ -217,7 +235,7 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
         if (!G || !pre_g || !pre_u) return fail(FP8G_ERR_NULL, "G, pre_g and pre_u are required");
         if ((st = check_rows("G", G, ldgrad, N, 2, &g_vec)) || (st = check_rows("pre_g", pre_g, ldp, N, 4, &p_vec)) ||
             (st = check_rows("pre_u", pre_u, ldp, N, 4, &p_vec2)) ||
-            (st = check_workspace(workspace, workspace_bytes, bf16_gated_nt_backward_workspace(M, N))))
+            (st = check_workspace(workspace, workspace_bytes, bf16_gated_nt_backward_workspace(M, N, K))))
             return st;
     }
     if (want_a) {
@@ -232,6 +250,7 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t cols = pad64(N);
     uint16_t *const w = static_cast<uint16_t *>(workspace);
+    float *const sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + grad_bytes(M, 2 * cols));
     if (M > 0 && N > 0) {
         GradParams g = {};
         g.G = static_cast<const uint16_t *>(G); g.ldg = ldgrad; g.g_vec = g_vec;
@@ -247,13 +266,13 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
         p.B2 = static_cast<const uint8_t *>(Wu);
         p.ksplit = (int)(cols / 64);
         p.krows = N;
-        if ((st = launch_backward<false, true>(p, 1, s))) return st;
+        if ((st = launch_backward<false, true>(p, 1, sums, s))) return st;
     }
     if (want_w) {
         FusedArgs p = base_args(w, 2 * cols, A, lda, dWg, lddw, N, K, M);
         p.D2 = static_cast<uint16_t *>(dWu);
         p.a_gstride = 2 * cols;
-        if ((st = launch_backward<true, true>(p, 2, s))) return st;
+        if ((st = launch_backward<true, true>(p, 2, sums, s))) return st;
     }
     return ok();
 }

@@ -79,7 +79,10 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
     const int rows_m = min(p.M - m0, BM), rows_n = min(p.N - n0, BNO);
     const int y = blockIdx.y;
     uint16_t *const d = y ? p.D2 : p.D;
-    const int nk = (p.K + KE - 1) / KE;
+    // this split's K steps: kb .. kb + nk - 1
+    constexpr bool SPLIT = EPI == EPI_PARTIAL;
+    const int kb = SPLIT ? (int)blockIdx.z * p.ksteps : 0;
+    const int nk = SPLIT ? min((p.K + KE - 1) / KE - kb, p.ksteps) : (p.K + KE - 1) / KE;
 
     // ---- copies ----
     // K-contiguous: copy qq fills ring rows 8 qq .. 8 qq + 7, lane l row l / 8,
@@ -124,25 +127,26 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
     const uint32_t bytes_b1 = rows_bytes(rows_n, p.ldb2);
     v4i srdA, srdB, srdB1 = {0, 0, 0, 0};
     uint32_t lds_a = 0, lds_b = 0, ko0 = 0, ko1 = 0;
-    auto set_step = [&](int kd) {
+    auto set_step = [&](int kd) {                  // the copies of local step kd follow
+        const int k = kb + kd;
+        const bool in = kd < nk;
         if constexpr (TA) {
-            srdA = make_srd(a0 + (int64_t)kd * KE * p.lda, rows_bytes(min(KE, p.K - kd * KE), p.lda));
+            srdA = make_srd(a0 + (int64_t)k * KE * p.lda, in ? rows_bytes(min(KE, p.K - k * KE), p.lda) : 0u);
         } else {
-            srdA = make_srd(a0 + (int64_t)kd * BK, kd < nk ? bytes_a - (uint32_t)(kd * BK) : 0u);
+            srdA = make_srd(a0 + (int64_t)k * BK, in ? bytes_a - (uint32_t)(k * BK) : 0u);
         }
         if constexpr (TB) {
-            const bool late = kd >= p.ksplit;
-            const int ks = late ? kd - p.ksplit : kd;
-            srdB = make_srd((late ? b1 : b0) + (int64_t)ks * KE * p.ldb,
-                            kd < nk ? rows_bytes(min(KE, p.krows - ks * KE), p.ldb) : 0u);
+            const bool late = k >= p.ksplit;
+            const int ks = late ? k - p.ksplit : k;
+            srdB = make_srd((late ? b1 : b0) + (int64_t)ks * KE * p.ldb, in ? rows_bytes(min(KE, p.krows - ks * KE), p.ldb) : 0u);
         } else {
-            srdB = make_srd(b0 + (int64_t)kd * BK, kd < nk ? bytes_b - (uint32_t)(kd * BK) : 0u);
-            if constexpr (GATED) srdB1 = make_srd(b1 + (int64_t)kd * BK, kd < nk ? bytes_b1 - (uint32_t)(kd * BK) : 0u);
+            srdB = make_srd(b0 + (int64_t)k * BK, in ? bytes_b - (uint32_t)(k * BK) : 0u);
+            if constexpr (GATED) srdB1 = make_srd(b1 + (int64_t)k * BK, in ? bytes_b1 - (uint32_t)(k * BK) : 0u);
         }
         lds_a = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)(wave * CPA) * 1024u;
         lds_b = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)BM * BK + (uint32_t)(wave * CPB) * 1024u;
         // K-contiguous: lanes whose chunk starts at or past K
-        const int lim = 2 * (p.K - kd * KE);
+        const int lim = 2 * (p.K - k * KE);
         ko0 = (int)kc0 < lim ? 0u : kOobOffset;
         ko1 = (int)kc1 < lim ? 0u : kOobOffset;
     };
@@ -376,6 +380,25 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams p) {
         const int c = blockIdx.y * 256 + tid;
         if (c < p.N) p.part[(int64_t)blockIdx.x * p.N + c] = total;
     }
+}
+
+// Outputs of a product split over K: the splits' sums added in split order,
+// rounded to BF16.  ws [splits][ny][M][N], N a multiple of 8; 8 columns per
+// thread, product y = blockIdx.y.
+__global__ __launch_bounds__(256) void join_kernel(const float *ws, int splits, int M, int N, uint16_t *d0, uint16_t *d1,
+                                                   int64_t ldd) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, out = (int64_t)M * N;
+    if (i >= out) return;
+    const float *src = ws + blockIdx.y * out + i;
+    const int64_t step = (int64_t)gridDim.y * out;
+    v4f lo = *reinterpret_cast<const v4f *>(src), hi = *reinterpret_cast<const v4f *>(src + 4);
+    for (int s = 1; s < splits; ++s) {
+        lo += *reinterpret_cast<const v4f *>(src + s * step);
+        hi += *reinterpret_cast<const v4f *>(src + s * step + 4);
+    }
+    uint16_t *const d = (blockIdx.y ? d1 : d0) + (i / N) * ldd + i % N;
+    const v2u a = pack_bf16x4(lo[0], lo[1], lo[2], lo[3]), b = pack_bf16x4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<v4u *>(d) = (v4u){a[0], a[1], b[0], b[1]};
 }
 
 // Column sums of part [rows][N], in row order.

@@ -21,7 +21,7 @@ int launch_tile(const FusedArgs &a, hipStream_t s) {
 
 template <int FA, int FB, int EPI>
 int launch_fmt(const FusedArgs &a, hipStream_t s) {
-    switch (pick_class(a.M, a.N, a.K, 1, EPI == EPI_GATED, true)) {
+    switch (pick_class(a.M, a.N, a.K, 1, EPI == EPI_GATED)) {
     case C_FEW: return launch_few_fmt<FA, FB, EPI>(a, s);
     case C_128x128: return launch_tile<128, 128, 4, FA, FB, EPI>(a, s);
     case C_128x256: return launch_tile<128, 256, 3, FA, FB, EPI>(a, s);
@@ -53,7 +53,14 @@ int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
     }
     if (m == 0 || n == 0) return ok();
     const bool gated = op == 1 || op == 3;
-    const ShapeClass c = pick_class(m, n, k, op < 2 ? 1 : 2, gated, op < 4);
+    ShapeClass c;
+    if (op == 4) {
+        const BackwardShape b = backward_shape(m, n, k, 1);
+        c = b.c;
+        out->k_splits = b.splits;
+    } else {
+        c = pick_class(m, n, k, op < 2 ? 1 : 2, gated);
+    }
     if (c == C_FEW) {
         const FewShape f = few_shape(m, n, gated);
         out->variant = 4;
@@ -66,7 +73,7 @@ int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
     out->variant = c == C_128x128 ? 7 : (c == C_128x256 ? 2 : 1);
     out->tile_m = c == C_256x256 ? 256 : 128;
     out->tile_n = (c == C_128x128 ? 128 : 256) / (gated ? 2 : 1);
-    out->workgroups = cdiv(m, out->tile_m) * cdiv(n, out->tile_n);
+    out->workgroups = cdiv(m, out->tile_m) * cdiv(n, out->tile_n) * out->k_splits;
     return ok();
 }
 

@@ -112,41 +112,75 @@ FewShape few_shape(int64_t M, int64_t N, bool gated) {
 // operands and the output.  The constants are fitted to 648 measured cases
 // (M 33 .. 4096 by nine N x K from 512 x 512 to 28672 x 512 and 1024 x 16384,
 // FP8 and BF16, fused, gated and both backward products, all four classes
-// each): on average the choice takes 0.5% longer than the fastest class.
+// each): on average the choice takes 0.2% longer than the fastest class.
 // Some: 512 x 4096 x 4096 FP8 38.4 / 17.7 / 29.1 / 45.6 us in the order of the
 // classes, 128 x 4096 x 4096 12.2 / 16.3 / 28.4 / 41.8, 2048 x 4096 x 4096
 // - / 43.1 / 34.9 / 47.7, 4096 x 4096 x 4096 - / 80.0 / 66.8 / 56.0.
 struct ClassCost {
     double launch, wave, step, load;
 };
-constexpr ClassCost kCost[2][3] = {{{1.8, 3.8, 0.29, 0.14}, {1.4, 6.1, 0.60, 0.15}, {0.1, 11.0, 0.93, 0.21}},
-                                   {{1.6, 4.1, 0.335, 0.144}, {0.9, 5.3, 0.58, 0.255}, {-0.7, 9.5, 0.97, 0.39}}};
+constexpr ClassCost kCost[2][3] = {{{1.7, 4.0, 0.29, 0.116}, {1.4, 6.1, 0.60, 0.117}, {0.5, 10.6, 0.93, 0.18}},
+                                   {{1.85, 4.0, 0.366, 0.095}, {2.3, 5.1, 0.663, 0.139}, {1.9, 9.0, 1.05, 0.21}}};
+constexpr int64_t kClassRows[3] = {128, 128, 256}, kClassCols[3] = {128, 256, 256};
+
+// us of a tiled kernel of class C_128x128 + c over `wgs` workgroups of `steps`
+// 128-byte K steps.
+double tiled_time(int c, int unit, int64_t wgs, int64_t steps) {
+    const ClassCost &k = kCost[unit - 1][c];
+    const double full = wgs < 256 ? (double)wgs / 256.0 : 1.0;
+    return k.launch + (double)cdiv(wgs, 256) * (k.wave + (double)steps * (k.step + k.load * full));
+}
 constexpr int64_t kFewMaxM = 512;
 
-// unit: bytes per element; few: the few-token kernel is a choice.
-ShapeClass pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated, bool few) {
+// unit: bytes per element.
+ShapeClass pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated) {
     const double kbytes = (double)K * unit;
     const int64_t cols = gated ? 2 * N : N;
     const double memory = 2.0 + (kbytes * ((double)cols + (double)M) + 2.0 * (double)M * (double)N) / 6.0e6;
     auto floored = [&](double t) { return (t > memory ? t : memory) + 0.05 * t; };
     ShapeClass best = C_256x256;
     double least = 1e300;
-    const int64_t rows[3] = {128, 128, 256}, width[3] = {128, 256, 256};
     for (int c = 0; c < 3; ++c) {
-        const int64_t wgs = cdiv(M, rows[c]) * cdiv(cols, width[c]);
-        const ClassCost &k = kCost[unit - 1][c];
-        const double full = wgs < 256 ? (double)wgs / 256.0 : 1.0;
-        const double t = floored(k.launch + (double)cdiv(wgs, 256) *
-                                                (k.wave + (double)cdiv(K * unit, 128) * (k.step + k.load * full)));
+        const double t = floored(tiled_time(c, unit, cdiv(M, kClassRows[c]) * cdiv(cols, kClassCols[c]), cdiv(K * unit, 128)));
         if (t < least) least = t, best = (ShapeClass)(C_128x128 + c);
     }
-    if (few && M <= kFewMaxM) {
+    if (M <= kFewMaxM) {
         const FewShape f = few_shape(M, N, gated);
         int fit = 160 * 1024 / (kFewWaves * (f.rb + f.cb) * 2048 * few_slots(f.rb, f.cb));
         if (fit > 3) fit = 3;
         double rounds = fit == 1 ? (double)cdiv(f.workgroups, 256) : (double)f.workgroups / 256.0;
         if (rounds < 1.0) rounds = 1.0;
-        if (floored(2.0 + rounds * (3.0 / fit + 16.0 * (f.rb + f.cb) * kbytes / 85e3)) <= least) best = C_FEW;
+        if (floored(2.0 + rounds * (2.0 / fit + 16.0 * (f.rb + f.cb) * kbytes / 85e3)) <= least) best = C_FEW;
+    }
+    return best;
+}
+
+// A BF16 backward product (ny of M x N outputs, N a multiple of 8, reduced over
+// K): its class, and the splits of K where the output has few tiles and K is
+// long.  The splits' FP32 sums are written to the workspace and joined by a
+// kernel of their own (3 us and the sums' way to memory and back), at most
+// kJoinBytes of them.
+struct BackwardShape {
+    ShapeClass c;
+    int splits, ksteps;
+    int64_t bytes;             // workspace of the sums
+};
+constexpr int64_t kJoinBytes = int64_t(128) << 20;
+
+BackwardShape backward_shape(int64_t M, int64_t N, int64_t K, int ny) {
+    BackwardShape best = {C_256x256, 1, 0, 0};
+    const int64_t steps = cdiv(2 * K, 128);
+    double least = 1e300;
+    for (int c = 0; c < 3; ++c) {
+        const int64_t tiles = cdiv(M, kClassRows[c]) * cdiv(N, kClassCols[c]) * ny;
+        for (int64_t want = 1; want <= 64; want *= 2) {
+            if (want > 1 && (tiles * want > 512 || steps < 2 * want)) break;
+            const int64_t per = steps ? cdiv(steps, want) : 0, splits = steps ? cdiv(steps, per) : 1;
+            const int64_t bytes = splits > 1 ? splits * ny * M * N * 4 : 0;
+            if (bytes > kJoinBytes) break;
+            const double t = tiled_time(c, 2, tiles * splits, per) + (splits > 1 ? 3.0 + (double)bytes / 2.0e6 : 0.0);
+            if (t < least) least = t, best = BackwardShape{(ShapeClass)(C_128x128 + c), (int)splits, (int)per, bytes};
+        }
     }
     return best;
 }

@@ -82,8 +82,10 @@ int bf16_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, c
  *   Each of dA, dB and dbias may be NULL (not computed).  ldda and lddb are
  *   multiples of 8; dA and dB 16-byte aligned.
  *   preact: Z, as kept by the forward call; NULL with FP8G_ACT_NONE only.
- *   workspace: at least bf16_gemm_nt_fused_backward_workspace(M, N) bytes,
- *   256-byte aligned; it holds dZ in BF16 and the bias gradient's partial sums.
+ *   workspace: at least bf16_gemm_nt_fused_backward_workspace(M, N, K) bytes,
+ *   256-byte aligned; it holds dZ in BF16, the bias gradient's partial sums and,
+ *   for products with few output tiles and a long sum, the FP32 sums of their
+ *   splits over K (added in split order).
  */
 int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64_t lda, const void *B, int64_t ldb,
                                 const float *preact, int64_t ldp, int activation,
@@ -91,7 +93,7 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
                                 void *workspace, int64_t workspace_bytes, int M, int N, int K, void *stream);
 
 /* Bytes of workspace of the call above (a negative fp8g_status for bad sizes). */
-int64_t bf16_gemm_nt_fused_backward_workspace(int M, int N);
+int64_t bf16_gemm_nt_fused_backward_workspace(int M, int N, int K);
 
 /*
  * Gated feed-forward product (both projections, activation and product in one
@@ -121,8 +123,8 @@ int bf16_gated_nt(const void *A, int64_t lda, const void *Wg, int64_t ldg, const
  *   dA = bf16_rne( dP . Wg + dU . Wu )                      [M][ldda]
  *   dWg = bf16_rne( dP^T . A ),  dWu = bf16_rne( dU^T . A )  [N][lddw] each
  *   dA may be NULL; so may dWg and dWu, together.
- *   workspace: at least bf16_gated_nt_backward_workspace(M, N) bytes, 256-byte
- *   aligned; it holds dP and dU in BF16.
+ *   workspace: at least bf16_gated_nt_backward_workspace(M, N, K) bytes,
+ *   256-byte aligned; it holds dP and dU in BF16 and the split sums, as above.
  */
 int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t lda, const void *Wg, int64_t ldg,
                            const void *Wu, int64_t ldu, const float *pre_g, const float *pre_u, int64_t ldp,
@@ -130,13 +132,13 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
                            void *workspace, int64_t workspace_bytes, int M, int N, int K, void *stream);
 
 /* Bytes of workspace of the call above (a negative fp8g_status for bad sizes). */
-int64_t bf16_gated_nt_backward_workspace(int M, int N);
+int64_t bf16_gated_nt_backward_workspace(int M, int N, int K);
 
 /*
  * Kernel choice for a problem, without launching anything (host only).
  *   op: 0 = fp8_gemm_nt_fused, 1 = fp8_gated_nt, 2 = bf16_gemm_nt_fused,
  *   3 = bf16_gated_nt, 4 = one BF16 backward product (m x n outputs, reduced
- *   over k; the gated weight gradients are one of 2 N x K).
+ *   over k), with k_splits splits of k.
  * Fills the plan of fp8_gemm.h: variant 1 = tiled 256 x 256, 2 = tiled 128 x
  * 256, 7 = tiled 128 x 128 (m x n of the products; the gated forms' tiles hold
  * half as many output columns), 4 = swapped decode, 0 = nothing to launch;

@@ -220,3 +220,29 @@ def test_every_gated_backward_class(f, M, N, K, va, vw):
     F.check(ga, *(x + y for x, y in zip(F.backward_products(dp, ep, wg), F.backward_products(du, eu, wu))), N, "grad_a")
     F.check(gg, *F.backward_products(dp.t(), ep.t(), a), M, "grad_gate")
     F.check(gu, *F.backward_products(du.t(), eu.t(), a), M, "grad_up")
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 9000, 264), (130, 4100, 136), (6000, 40, 136), (9000, 130, 520), (12000, 1030, 1032)])
+def test_split_backward_products(f, M, N, K):
+    """Few output tiles and a long sum: K split over workgroups, for grad_a (reduced over N) or the weights' (over M)."""
+    cols = (N + 63) // 64 * 64
+    splits = f.fused_plan(4, M, K, cols).k_splits, f.fused_plan(4, N, K, M).k_splits
+    assert max(splits) > 1
+    a, b, u, G = rand(1, M, K), rand(2, N, K, std=0.25), rand(5, N, K, std=0.25), rand(3, M, N)
+    pre = rand(4, 2 * M, N, dtype=torch.float32).view(2, M, N)
+    g64, (z, w) = G.cpu().double(), pre.cpu().double()
+    v, dv = F.act("silu", z)
+    zero = torch.zeros_like(z)
+    ga, gb, _ = f.gemm_nt_bf16_fused_backward(G, a, b, "silu", pre[0])
+    dz, err = g64 * dv, grad_error("silu", g64, z, zero)
+    F.check(ga, *F.backward_products(dz, err, b), N, "grad_a")
+    F.check(gb, *F.backward_products(dz.t(), err.t(), a), M, "grad_b")
+    for _ in range(3):
+        again = f.gemm_nt_bf16_fused_backward(G, a, b, "silu", pre[0])
+        assert torch.equal(again[0], ga) and torch.equal(again[1], gb)
+    ga, gg, gu = f.gated_nt_bf16_backward(G, a, b, u, pre)
+    dp, du = g64 * w * dv, g64 * v
+    ep, eu = grad_error("silu", g64 * w, z, zero), g64.abs() * 2.0 ** -19 * z.abs()
+    F.check(ga, *(x + y for x, y in zip(F.backward_products(dp, ep, b), F.backward_products(du, eu, u))), N, "grad_a")
+    F.check(gg, *F.backward_products(dp.t(), ep.t(), a), M, "grad_gate")
+    F.check(gu, *F.backward_products(du.t(), eu.t(), a), M, "grad_up")

@@ -132,12 +132,29 @@ def test_nothing_to_launch(f):
 
 def test_workspaces(f):
     lib = f.load_library()
-    for M, N in ((0, 0), (1, 1), (64, 64), (65, 129), (4096, 14336)):
+    for M, N, K in ((0, 0, 0), (1, 1, 8), (64, 64, 64), (65, 129, 1000), (5, 14336, 4096), (8192, 128, 128), (4096, 14336, 4096)):
         cols = (N + 63) // 64 * 64
-        assert lib.bf16_gated_nt_backward_workspace(M, N) >= 4 * M * cols
-        assert lib.bf16_gemm_nt_fused_backward_workspace(M, N) >= 2 * M * cols + 4 * ((M + 63) // 64) * N
-    assert lib.bf16_gated_nt_backward_workspace(-1, 4) == -2
-    assert lib.bf16_gemm_nt_fused_backward_workspace(4, 1 << 22) == -2
+        # the gradients, the bias sums, and what the split products need
+        sums = [0]
+        if K:
+            for m, k in ((M, cols), (N, M)):
+                splits = f.fused_plan(4, m, K, k).k_splits
+                sums.append(4 * splits * m * K if splits > 1 else 0)
+        need = 2 * M * cols + 4 * ((M + 63) // 64) * N + max(sums)
+        assert lib.bf16_gemm_nt_fused_backward_workspace(M, N, K) >= need
+        assert lib.bf16_gated_nt_backward_workspace(M, N, K) >= 4 * M * cols
+    assert lib.bf16_gated_nt_backward_workspace(-1, 4, 8) == -2
+    assert lib.bf16_gemm_nt_fused_backward_workspace(4, 1 << 22, 8) == -2
+    assert lib.bf16_gemm_nt_fused_backward_workspace(4, 4, 4) == -2
+
+
+@pytest.mark.parametrize("m,n,k,splits", [(4096, 4096, 4096, False), (5, 1000, 14336, True), (128, 128, 8192, True),
+                                          (1024, 1024, 65536, True), (64, 64, 64, False), (24, 712, 962, True)])
+def test_backward_splits(f, m, n, k, splits):
+    p = f.fused_plan(4, m, n, k)
+    assert (p.k_splits > 1) == splits
+    assert p.workgroups == -(-m // p.tile_m) * -(-n // p.tile_n) * p.k_splits
+    assert p.k_splits <= 64 and 4 * p.k_splits * m * n <= 128 << 20
 
 
 @pytest.mark.parametrize("op,m,n,k,variant", [
@@ -147,11 +164,11 @@ def test_workspaces(f):
 ])
 def test_plan(f, op, m, n, k, variant):
     p = f.fused_plan(op, m, n, k)
-    assert p.variant == variant and p.k_splits == 1
+    assert p.variant == variant
     if variant == 4:
         assert p.workgroups == -(-n // p.tile_n) * -(-m // 64)
     elif variant:
-        assert p.workgroups == -(-m // p.tile_m) * -(-n // p.tile_n)
+        assert p.workgroups == -(-m // p.tile_m) * -(-n // p.tile_n) * p.k_splits
 
 
 @pytest.mark.parametrize("op,m,n,k,status", [(5, 1, 1, 16, -8), (-1, 1, 1, 16, -8), (0, 1, 1, 8, -2), (2, 1, 1, 4, -2), (0, -1, 1, 16, -2)])
