@@ -76,7 +76,14 @@ int64_t pad256(int64_t n) { return (n + 255) / 256 * 256; }
 // K] reduced over `cols`, nw weight gradients [N x K] reduced over M), which
 // follow one another.
 int64_t grad_bytes(int64_t M, int64_t cols) { return pad256(2 * M * cols); }
-int64_t bias_bytes(int64_t M, int64_t N) { return pad256(4 * cdiv(M, fp8g::kGradRows) * N); }
+// Rows per block of the pre-activation gradients: 64, or fewer while there
+// are not 1024 blocks.
+int grad_rows(int64_t M, int64_t cols) {
+    int rows = fp8g::kGradMaxRows;
+    while (rows > 8 && cdiv(M, rows) * cdiv(cols, 256) < 1024) rows /= 2;
+    return rows;
+}
+int64_t bias_bytes(int64_t M, int64_t N) { return pad256(4 * cdiv(M, grad_rows(M, pad64(N))) * N); }
 int64_t join_bytes(int64_t M, int64_t N, int64_t K, int64_t cols, int nw) {
     if (K == 0) return 0;
     const int64_t a = backward_shape(M, K, cols, 1).bytes, w = backward_shape(N, K, M, nw).bytes;
@@ -101,8 +108,9 @@ int check_grad_sizes(int M, int N) {
 }
 
 template <bool GATED, bool BIAS>
-int launch_grad(const GradParams &g, int cols, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(g.M, fp8g::kGradRows), (unsigned)cdiv(cols, 256));
+int launch_grad(GradParams g, int cols, hipStream_t s) {
+    g.rows = grad_rows(g.M, cols);
+    const dim3 grid((unsigned)cdiv(g.M, g.rows), (unsigned)cdiv(cols, 256));
     hipLaunchKernelGGL((fp8g::grad_kernel<GATED, BIAS>), grid, dim3(256), 0, s, g);
     return launch_status("pre-activation gradient kernel");
 }
@@ -176,8 +184,8 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
         if (st) return st;
     }
     if (dbias && N > 0) {
-        hipLaunchKernelGGL(fp8g::bias_grad_kernel, dim3((unsigned)cdiv(N, 256)), dim3(256), 0, s, part,
-                           (int)cdiv(M, fp8g::kGradRows), N, dbias);
+        hipLaunchKernelGGL(fp8g::bias_grad_kernel, dim3((unsigned)cdiv(N, 32)), dim3(256), 0, s, part,
+                           (int)cdiv(M, grad_rows(M, cols)), N, dbias);
         if ((st = launch_status("bias gradient kernel"))) return st;
     }
     const void *dz = direct ? G : w;

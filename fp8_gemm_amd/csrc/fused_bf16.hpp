@@ -309,9 +309,12 @@ __device__ __forceinline__ float act_value_exact(float z) {
 // element (fused), 10 and 4 (gated).
 // BIAS: also the column sums of the FP32 dZ over the block's rows into
 // part[block row][N], added over the rows in a fixed order.
-// A block is 32 groups of 8 columns x 8 rows of threads, kGradRows rows.
+// A block is 32 groups of 8 columns x 8 rows of threads over `rows` rows: as
+// few as 8 where M x N is small, so that every row's loads are in flight at
+// once (301 x 1111, unaligned rows: 25.7 us with 64 rows per block, which 25
+// blocks ran through 8 at a time).
 // ---------------------------------------------------------------------------
-constexpr int kGradRows = 64;
+constexpr int kGradMaxRows = 64;
 
 struct GradParams {
     const uint16_t *G;         // output gradient [M][ldg] BF16
@@ -319,7 +322,7 @@ struct GradParams {
     uint16_t *W;               // NULL: column sums only
     float *part;
     int64_t ldg, ldp, ldw;
-    int M, N, act, g_vec, p_vec;
+    int M, N, act, g_vec, p_vec, rows;
 };
 
 __device__ __forceinline__ void load_f32_row8(const float *src, int nv, bool vec, float (&out)[8]) {
@@ -341,34 +344,34 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams p) {
     const int nv = p.N - n;                        // <= 0: padding columns
     const int half = GATED ? (int)(p.ldw / 2) : (int)p.ldw;   // columns of W per matrix
     float bsum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const int r0 = blockIdx.x * kGradRows;
+    const int r0 = blockIdx.x * p.rows, r1 = min(p.M, r0 + p.rows);
     with_activation(p.act, [&](auto act) {
-    for (int r = r0 + (tid >> 5); r < min(p.M, r0 + kGradRows); r += 8) {
-        float g[8], z[8], z2[8], dz[8], du[8];
-        load_bf16_row<8>(p.G + (int64_t)r * p.ldg + n, nv, p.g_vec, g);
-        if (GATED || act.value != ACT_NONE) load_f32_row8(p.pre + (int64_t)r * p.ldp + n, nv, p.p_vec, z);
-        if (GATED) load_f32_row8(p.pre2 + (int64_t)r * p.ldp + n, nv, p.p_vec, z2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (e >= nv) {                         // (a padding column is zero whatever its gradient)
-                dz[e] = du[e] = 0.0f;
-            } else if (GATED) {
-                dz[e] = g[e] * z2[e] * act_slope<act.value>(z[e]);
-                du[e] = g[e] * act_value_exact<act.value>(z[e]);
-            } else {
-                dz[e] = act.value != ACT_NONE ? g[e] * act_slope<act.value>(z[e]) : g[e];
+        for (int r = r0 + (tid >> 5); r < r1; r += 8) {
+            float g[8], z[8], z2[8], dz[8], du[8];
+            load_bf16_row<8>(p.G + (int64_t)r * p.ldg + n, nv, p.g_vec, g);
+            if (GATED || act.value != ACT_NONE) load_f32_row8(p.pre + (int64_t)r * p.ldp + n, nv, p.p_vec, z);
+            if (GATED) load_f32_row8(p.pre2 + (int64_t)r * p.ldp + n, nv, p.p_vec, z2);
+    #pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e >= nv) {                         // (a padding column is zero whatever its gradient)
+                    dz[e] = du[e] = 0.0f;
+                } else if (GATED) {
+                    dz[e] = g[e] * z2[e] * act_slope<act.value>(z[e]);
+                    du[e] = g[e] * act_value_exact<act.value>(z[e]);
+                } else {
+                    dz[e] = act.value != ACT_NONE ? g[e] * act_slope<act.value>(z[e]) : g[e];
+                }
+                if (BIAS) bsum[e] += dz[e];
             }
-            if (BIAS) bsum[e] += dz[e];
-        }
-        if (p.W && n < half) {                     // (half is a multiple of 64: whole groups)
-            const v2u lo = pack_bf16x4(dz[0], dz[1], dz[2], dz[3]), hi = pack_bf16x4(dz[4], dz[5], dz[6], dz[7]);
-            *reinterpret_cast<v4u *>(p.W + (int64_t)r * p.ldw + n) = (v4u){lo[0], lo[1], hi[0], hi[1]};
-            if (GATED) {
-                const v2u l2 = pack_bf16x4(du[0], du[1], du[2], du[3]), h2 = pack_bf16x4(du[4], du[5], du[6], du[7]);
-                *reinterpret_cast<v4u *>(p.W + (int64_t)r * p.ldw + half + n) = (v4u){l2[0], l2[1], h2[0], h2[1]};
+            if (p.W && n < half) {                     // (half is a multiple of 64: whole groups)
+                const v2u lo = pack_bf16x4(dz[0], dz[1], dz[2], dz[3]), hi = pack_bf16x4(dz[4], dz[5], dz[6], dz[7]);
+                *reinterpret_cast<v4u *>(p.W + (int64_t)r * p.ldw + n) = (v4u){lo[0], lo[1], hi[0], hi[1]};
+                if (GATED) {
+                    const v2u l2 = pack_bf16x4(du[0], du[1], du[2], du[3]), h2 = pack_bf16x4(du[4], du[5], du[6], du[7]);
+                    *reinterpret_cast<v4u *>(p.W + (int64_t)r * p.ldw + half + n) = (v4u){l2[0], l2[1], h2[0], h2[1]};
+                }
             }
         }
-    }
     });
     if constexpr (BIAS) {
 #pragma unroll
@@ -401,12 +404,28 @@ __global__ __launch_bounds__(256) void join_kernel(const float *ws, int splits, 
     *reinterpret_cast<v4u *>(d) = (v4u){a[0], a[1], b[0], b[1]};
 }
 
-// Column sums of part [rows][N], in row order.
+// Column sums of part [rows][N]: 32 columns per block, 8 threads per column
+// over every 8th row, their sums added in order.
 __global__ __launch_bounds__(256) void bias_grad_kernel(const float *part, int rows, int n, float *out) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
+    __shared__ float sums[8][32];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     float total = 0.0f;
-    for (int r = 0; r < rows; ++r) total += part[(int64_t)r * n + c];
+    if (c < n) {
+        int r = lane;
+        for (; r + 24 < rows; r += 32) {           // four rows' loads at a time
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = part[(int64_t)(r + 8 * k) * n + c];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) total += v[k];
+        }
+        for (; r < rows; r += 8) total += part[(int64_t)r * n + c];
+    }
+    sums[lane][threadIdx.x & 31] = total;
+    __syncthreads();
+    if (lane || c >= n) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) total += sums[k][threadIdx.x];
     out[c] = total;
 }
 

@@ -92,7 +92,7 @@ def test_gradients_on_request(f):
         g64 = G[:, :n].cpu().double()
         F.check(ga, *F.backward_products(g64, torch.zeros_like(g64), b[:n]), n, "grad_a")
         F.check(gb, *F.backward_products(g64.t(), torch.zeros_like(g64).t(), a), M, "grad_b")
-        assert ((gbias.cpu().double() - g64.sum(0)).abs() <= 20 * 2.0 ** -24 * g64.abs().sum(0)).all()
+        assert ((gbias.cpu().double() - g64.sum(0)).abs() <= 34 * 2.0 ** -24 * g64.abs().sum(0)).all()   # depth M / 64 + 32
     pre2 = torch.empty(2, M, N, device=DEV)
     f.gated_nt_bf16(a, b, u, preact=pre2)
     full = f.gated_nt_bf16_backward(G, a, b, u, pre2)
