@@ -18,7 +18,10 @@ int launch_shape(const FusedArgs &a, int ny, int splits, hipStream_t s) {
     p.tiles_m = (int)cdiv(p.M, BM);
     p.tiles_n = (int)cdiv(p.N, EPI == EPI_GATED ? BN / 2 : BN);
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)ny, (unsigned)splits), block(256);
-    hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, STAGES, TA, TB, EPI>), grid, block, 0, s, p);
+    if (!(TA && TB) && p.K % 64)
+        hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, STAGES, TA, TB, !(TA && TB), EPI>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((fp8g::bf16_tile_kernel<BM, BN, STAGES, TA, TB, false, EPI>), grid, block, 0, s, p);
     return launch_status("fused BF16 tiled kernel");
 }
 

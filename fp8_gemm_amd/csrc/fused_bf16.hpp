@@ -12,9 +12,23 @@ namespace fp8g {
 // ---------------------------------------------------------------------------
 // BF16 tiled kernel.  BM x BN outputs per workgroup of 4 waves (2 x 2) on
 // v_mfma 16x16x32, K in steps of 64 elements through a direct-to-LDS ring of
-// STAGES slots: fragments read one K half (32 elements) ahead of the matrix
-// instructions, one barrier per step, the refill of a step's slot spread over
-// the second half's instructions.
+// STAGES slots.  A step is two K halves (32 elements, one instruction per block
+// pair) of T / 2 matrix instructions each:
+//   - 0 .. T / 4: the fragments of the step's second half are read;
+//   - barrier A, at 17 T / 64: everyone has read the step's slot, and its
+//     refill (step kt + STAGES) is spread over the rest of the step;
+//   - barrier B, at 5 T / 8: step kt + 1 has landed for everyone, and its first
+//     half's fragments are read up to the step's end.
+// With two slots a step's copies thus have 5 T / 8 instructions or more to land
+// and go out over 47 T / 64 of them; one barrier in the middle of the step, for
+// both, left T / 2 and T / 2.  The loop waits on its copies (in that form 4096 x
+// 4096 x 16384 took 448 us, 326 without the loop's copies, 444 without its
+// fragment reads), and the more evenly they go out the less: 4096^3 103.2 ->
+// 99.7 us; token gradient of the gated 4096 x 14336 x 4096 851 (one barrier),
+// 848 (copies over T / 2 from A on) -> 811 us (to the end), weight gradients
+// 908, 929 -> 900 us.  Steps of 32 elements with twice the slots measured 8%
+// slower than the one-barrier form on K-contiguous operands, whose rows are
+// then fetched half a cache line at a time, and no faster on K-strided ones.
 //
 // Either operand may be K-contiguous (rows of K elements: ring rows of 128
 // bytes, read with ds_read_b128; 16-byte chunk c of row r stored at c ^ ((r >>
@@ -48,7 +62,8 @@ __device__ __forceinline__ v2u lds_read_tr16(const uint8_t *a) {
     return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)a));
 }
 
-template <int BM, int BN, int STAGES, bool TA, bool TB, int EPI>
+// TAIL: a K-contiguous operand whose K is not a multiple of 64.
+template <int BM, int BN, int STAGES, bool TA, bool TB, bool TAIL, int EPI>
 __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, false> p) {
     constexpr bool GATED = EPI == EPI_GATED;
     static_assert(!GATED || (!TA && !TB), "gated: K-contiguous operands");
@@ -146,14 +161,16 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
         lds_a = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)(wave * CPA) * 1024u;
         lds_b = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)BM * BK + (uint32_t)(wave * CPB) * 1024u;
         // K-contiguous: lanes whose chunk starts at or past K
-        const int lim = 2 * (p.K - k * KE);
-        ko0 = (int)kc0 < lim ? 0u : kOobOffset;
-        ko1 = (int)kc1 < lim ? 0u : kOobOffset;
+        if constexpr (TAIL) {
+            const int lim = 2 * (p.K - k * KE);
+            ko0 = (int)kc0 < lim ? 0u : kOobOffset;
+            ko1 = (int)kc1 < lim ? 0u : kOobOffset;
+        }
     };
     auto issue_one = [&](int i) {
         const uint32_t ko = (i & 1) ? ko1 : ko0;   // (CPA is even)
-        if (i < CPA) dma16_m0(srdA, TA ? lo_a[i] : lo_a[i] + ko, lds_a + (uint32_t)i * 1024u);
-        else dma16_m0(GATED && ((i - CPA) & 2) ? srdB1 : srdB, TB ? lo_b[i - CPA] : lo_b[i - CPA] + ko,
+        if (i < CPA) dma16_m0(srdA, TA || !TAIL ? lo_a[i] : lo_a[i] + ko, lds_a + (uint32_t)i * 1024u);
+        else dma16_m0(GATED && ((i - CPA) & 2) ? srdB1 : srdB, TB || !TAIL ? lo_b[i - CPA] : lo_b[i - CPA] + ko,
                       lds_b + (uint32_t)(i - CPA) * 1024u);
     };
 
@@ -193,30 +210,50 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
 #pragma unroll
         for (int j = 0; j < FM; ++j) acc[i][j] = (v4f){0, 0, 0, 0};
 
-    // One K half of matrix instructions, with the next half's fragment reads
-    // and, in the second half, the refill of the step's slot spread between
-    // them.  (Unrolled by the template: the loop pragma gave up on K-strided
-    // operands.)
-    constexpr int NMF = FN * FM, NFR = FN + FM;
-    auto half_step = [&](const v4u (&bf)[FN], const v4u (&af)[FM], v4u (&nb)[FN], v4u (&na)[FM], const uint8_t *read_slot,
-                         int read_h, int refill) {
-        static_for<NMF>([&](auto tc) {
-            constexpr int t = tc.value, i = t / FM, j = t % FM;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, bf[i]),
-                                                                __builtin_bit_cast(v8bf, af[j]), acc[i][j], 0, 0, 0);
+    // One K step (see above).  (Unrolled by the template: the loop pragma gave
+    // up on K-strided operands.)
+    constexpr int NMF = FN * FM, NFR = FN + FM, T = 2 * NMF;
+    constexpr int kRead1 = T / 4, kBarA = 17 * T / 64, kCopyTo = T, kBarB = 5 * T / 8;
+    static_assert(kRead1 <= kBarA && kBarA < NMF && kBarB >= NMF && kCopyTo <= T, "schedule");
+    // copies out at barrier B: those issued from barrier A on
+    constexpr int kIssued = ((kBarB - kBarA) * CPW) / (kCopyTo - kBarA);
+    static_assert(CPW * (STAGES - 2) + kIssued < 64, "copies in flight");
+    v4u f0b[FN], f0a[FM], f1b[FN], f1a[FM];
+    auto step = [&](int kt) {
+        const uint8_t *cur = smem + (kt % STAGES) * SLOT;
+        const uint8_t *nxt = smem + ((kt + 1) % STAGES) * SLOT;
+        static_for<T>([&](auto tc) {
+            constexpr int t = tc.value, i = (t % NMF) / FM, j = (t % NMF) % FM;
+            if constexpr (t == kBarA) {
+                __syncthreads();                   // step kt's slot is no longer read
+                set_step(kt + STAGES);
+            }
+            if constexpr (t == kBarB) {
+                vmcnt_wait<CPW * (STAGES - 2) + kIssued>();   // this wave's part of step kt + 1 has landed
+                __syncthreads();                   // everyone's has
+            }
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, t < NMF ? f0b[i] : f1b[i]),
+                                                                __builtin_bit_cast(v8bf, t < NMF ? f0a[j] : f1a[j]),
+                                                                acc[i][j], 0, 0, 0);
+            if constexpr (t < kRead1) {
 #pragma unroll
-            for (int q = (t * NFR) / NMF; q < ((t + 1) * NFR) / NMF; ++q) read_frag(nb, na, read_slot, read_h, q);
-            if (refill >= 0) {
-                if (t == 0) set_step(refill);
+                for (int q = (t * NFR) / kRead1; q < ((t + 1) * NFR) / kRead1; ++q) read_frag(f1b, f1a, cur, 1, q);
+            }
+            if constexpr (t >= kBarA && t < kCopyTo) {
 #pragma unroll
-                for (int q = (t * CPW) / NMF; q < ((t + 1) * CPW) / NMF; ++q) issue_one(q);
+                for (int q = ((t - kBarA) * CPW) / (kCopyTo - kBarA); q < ((t - kBarA + 1) * CPW) / (kCopyTo - kBarA); ++q)
+                    issue_one(q);
+            }
+            if constexpr (t >= kBarB) {
+#pragma unroll
+                for (int q = ((t - kBarB) * NFR) / (T - kBarB); q < ((t - kBarB + 1) * NFR) / (T - kBarB); ++q)
+                    read_frag(f0b, f0a, nxt, 0, q);
             }
             __builtin_amdgcn_sched_barrier(0);
         });
     };
 
     if constexpr (EPI == EPI_ACT) copy_tile_terms(p, smem + RING, lds0 + (uint32_t)RING, wave, lane, m0, rows_m, n0, rows_n);
-    v4u f0b[FN], f0a[FM], f1b[FN], f1a[FM];
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
         set_step(s);
@@ -228,13 +265,8 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
 #pragma unroll
     for (int q = 0; q < NFR; ++q) read_frag(f0b, f0a, smem, 0, q);
     for (int kt = 0; kt < nk; ++kt) {
-        const uint8_t *cur = smem + (kt % STAGES) * SLOT;
-        const uint8_t *nxt = smem + ((kt + 1) % STAGES) * SLOT;
         __builtin_amdgcn_sched_barrier(0);
-        half_step(f0b, f0a, f1b, f1a, cur, 1, -1);
-        vmcnt_wait<CPW * (STAGES - 2)>();          // this wave's part of step kt + 1 has landed
-        __syncthreads();                           // everyone's has; step kt's slot is no longer read
-        half_step(f1b, f1a, f0b, f0a, nxt, 0, kt + STAGES);
+        step(kt);
     }
     vmcnt_wait<0>();                               // drain the copies past the last step
     __syncthreads();                               // every wave's have landed; the ring is free
