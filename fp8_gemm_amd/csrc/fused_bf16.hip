@@ -36,12 +36,12 @@ int launch_tile(ShapeClass c, const FusedArgs &a, int ny, int splits, hipStream_
 // strides in bytes, the tiled kernel K in elements.
 template <int EPI>
 int launch_forward(FusedArgs p, hipStream_t s) {
-    const ShapeClass c = pick_class(p.M, p.N, p.K, 2, EPI == EPI_GATED);
-    if (c == C_FEW) {
+    const Choice c = pick_class(p.M, p.N, p.K, 2, EPI == EPI_GATED);
+    if (c.c == C_FEW) {
         p.K *= 2;
-        return launch_few_fmt<FMT_BF16, FMT_BF16, EPI>(p, s);
+        return launch_few_fmt<FMT_BF16, FMT_BF16, EPI>(p, c.few, s);
     }
-    return launch_tile<false, false, EPI>(c, p, 1, 1, s);
+    return launch_tile<false, false, EPI>(c.c, p, 1, 1, s);
 }
 
 // A backward product (ny of them), its split sums in `sums`.

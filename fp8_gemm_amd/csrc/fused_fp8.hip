@@ -21,8 +21,9 @@ int launch_tile(const FusedArgs &a, hipStream_t s) {
 
 template <int FA, int FB, int EPI>
 int launch_fmt(const FusedArgs &a, hipStream_t s) {
-    switch (pick_class(a.M, a.N, a.K, 1, EPI == EPI_GATED)) {
-    case C_FEW: return launch_few_fmt<FA, FB, EPI>(a, s);
+    const Choice c = pick_class(a.M, a.N, a.K, 1, EPI == EPI_GATED);
+    switch (c.c) {
+    case C_FEW: return launch_few_fmt<FA, FB, EPI>(a, c.few, s);
     case C_128x128: return launch_tile<128, 128, 4, FA, FB, EPI>(a, s);
     case C_128x256: return launch_tile<128, 256, 3, FA, FB, EPI>(a, s);
     default: return launch_tile<256, 256, 2, FA, FB, EPI>(a, s);
@@ -59,16 +60,17 @@ int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
         c = b.c;
         out->k_splits = b.splits;
     } else {
-        c = pick_class(m, n, k, op < 2 ? 1 : 2, gated);
-    }
-    if (c == C_FEW) {
-        const FewShape f = few_shape(m, n, gated);
-        out->variant = 4;
-        out->tile_m = 16 * f.cb;
-        out->tile_n = gated ? 8 * f.rb : 16 * f.rb;
-        out->token_blocks = f.cb;
-        out->workgroups = f.workgroups;
-        return ok();
+        const Choice choice = pick_class(m, n, k, op < 2 ? 1 : 2, gated);
+        c = choice.c;
+        if (c == C_FEW) {
+            const FewShape &f = choice.few;
+            out->variant = 4;
+            out->tile_m = 16 * f.cb;
+            out->tile_n = gated ? 8 * f.rb : 16 * f.rb;
+            out->token_blocks = f.cb;
+            out->workgroups = f.workgroups;
+            return ok();
+        }
     }
     out->variant = c == C_128x128 ? 7 : (c == C_128x256 ? 2 : 1);
     out->tile_m = c == C_256x256 ? 256 : 128;

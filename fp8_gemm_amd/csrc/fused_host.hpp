@@ -92,35 +92,35 @@ struct FewShape {
 constexpr int kFewWaves = 4;
 constexpr int few_slots(int rb, int cb) { return rb == 1 && cb == 1 ? 3 : 2; }
 
-// Twice the weight rows per workgroup where that still leaves two workgroups
-// per CU: half the token copies per weight row.
-FewShape few_shape(int64_t M, int64_t N, bool gated) {
+FewShape few_shape(int64_t M, int64_t N, bool gated, int rb) {
     FewShape f;
-    const int r0 = gated ? 2 : 1;
-    f.rb = cdiv(N, gated ? 16 : 32) >= 512 ? 2 * r0 : r0;
+    f.rb = rb;
     f.cb = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-    f.workgroups = cdiv(N, gated ? 8 * f.rb : 16 * f.rb) * cdiv(M, 64);
+    f.workgroups = cdiv(N, gated ? 8 * rb : 16 * rb) * cdiv(M, 64);
     return f;
 }
 
 // The class with the smallest estimated time in us.  A tiled kernel's: a
 // launch, and per wave of 256 workgroups (one per CU) a fixed part (prologue
 // and epilogue) and its 128-byte K steps, each the slower the more CUs work
-// (clock and memory); the few-token kernel's: its rounds of workgroups, each a
-// fixed part shared by the workgroups that fit a CU and the bytes that its
-// copies bring in; all of them at least the time that memory takes for the
-// operands and the output.  The constants are fitted to 648 measured cases
-// (M 33 .. 4096 by nine N x K from 512 x 512 to 28672 x 512 and 1024 x 16384,
-// FP8 and BF16, fused, gated and both backward products, all four classes
-// each): on average the choice takes 0.2% longer than the fastest class.
-// Some: 512 x 4096 x 4096 FP8 38.4 / 17.7 / 29.1 / 45.6 us in the order of the
-// classes, 128 x 4096 x 4096 12.2 / 16.3 / 28.4 / 41.8, 2048 x 4096 x 4096
-// - / 43.1 / 34.9 / 47.7, 4096 x 4096 x 4096 - / 80.0 / 66.8 / 56.0.
+// (clock and memory); the few-token kernel's, for each number of weight rows
+// per workgroup (more rows: fewer copies of the tokens, fewer workgroups): its
+// rounds of workgroups, each a fixed part shared by the workgroups that fit a
+// CU and the bytes that its copies bring in; all of them at least the time
+// that memory takes for the operands and the output.  The constants are fitted
+// to 540 measured cases (M 1 .. 2048 by nine N x K from 512 x 512 to 28672 x
+// 1024 and 1024 x 8192, FP8 and BF16, fused and gated, every class each, the
+// weights read from memory as a serving pass does): on average the choice
+// takes 0.7% longer than the fastest class.  Some, FP8 fused, few-token with
+// 16, 32 and 64 rows | 128 x 128 | 128 x 256 tiles, in us: 64 x 14336 x 4096
+// 24.7, 20.7, 17.2 | 22.1 | 32.4; 256 x 4096 x 14336 61.1, 42.3, 33.3 | 72.0 |
+// 99.2; 512 x 4096 x 4096 36.9, 28.8, 21.7 | 23.1 | 33.2; 64 x 4096 x 4096
+// 8.8, 10.3, - | 19.9 | 30.8.
 struct ClassCost {
     double launch, wave, step, load;
 };
-constexpr ClassCost kCost[2][3] = {{{1.7, 4.0, 0.29, 0.116}, {1.4, 6.1, 0.60, 0.117}, {0.5, 10.6, 0.93, 0.18}},
-                                   {{1.85, 4.0, 0.366, 0.095}, {2.3, 5.1, 0.663, 0.139}, {1.9, 9.0, 1.05, 0.21}}};
+constexpr ClassCost kCost[2][3] = {{{1.6, 3.3, 0.416, 0.19}, {1.6, 5.4, 0.696, 0.219}, {0.9, 8.3, 1.266, 0.405}},
+                                   {{2.0, 3.1, 0.416, 0.16}, {2.1, 4.6, 0.708, 0.191}, {-0.6, 11.0, 1.026, 0.258}}};
 constexpr int64_t kClassRows[3] = {128, 128, 256}, kClassCols[3] = {128, 256, 256};
 
 // us of a tiled kernel of class C_128x128 + c over `wgs` workgroups of `steps`
@@ -130,27 +130,36 @@ double tiled_time(int c, int unit, int64_t wgs, int64_t steps) {
     const double full = wgs < 256 ? (double)wgs / 256.0 : 1.0;
     return k.launch + (double)cdiv(wgs, 256) * (k.wave + (double)steps * (k.step + k.load * full));
 }
-constexpr int64_t kFewMaxM = 512;
+
+constexpr int64_t kFewMaxM = 2048;                 // (its 64-token tiles re-read the weights from the caches)
+
+struct Choice {
+    ShapeClass c;
+    FewShape few;              // C_FEW
+};
 
 // unit: bytes per element.
-ShapeClass pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated) {
+Choice pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated) {
     const double kbytes = (double)K * unit;
     const int64_t cols = gated ? 2 * N : N;
-    const double memory = 2.0 + (kbytes * ((double)cols + (double)M) + 2.0 * (double)M * (double)N) / 6.0e6;
+    const double memory = 2.0 + (kbytes * ((double)cols + (double)M) + 2.0 * (double)M * (double)N) / 5.0e6;
     auto floored = [&](double t) { return (t > memory ? t : memory) + 0.05 * t; };
-    ShapeClass best = C_256x256;
+    Choice best = {C_256x256, {}};
     double least = 1e300;
+    if (M <= kFewMaxM) {
+        for (int rb = gated ? 2 : 1; rb <= 4; rb *= 2) {
+            const FewShape f = few_shape(M, N, gated, rb);
+            int fit = 160 * 1024 / (kFewWaves * (f.rb + f.cb) * 2048 * few_slots(f.rb, f.cb));
+            if (fit > 3) fit = 3;
+            double rounds = fit == 1 ? (double)cdiv(f.workgroups, 256) : (double)f.workgroups / 256.0;
+            if (rounds < 1.0) rounds = 1.0;
+            const double t = floored(2.5 + rounds * (1.5 / fit + 16.0 * (f.rb + f.cb) * kbytes / 70e3));
+            if (t < least) least = t, best = Choice{C_FEW, f};
+        }
+    }
     for (int c = 0; c < 3; ++c) {
         const double t = floored(tiled_time(c, unit, cdiv(M, kClassRows[c]) * cdiv(cols, kClassCols[c]), cdiv(K * unit, 128)));
-        if (t < least) least = t, best = (ShapeClass)(C_128x128 + c);
-    }
-    if (M <= kFewMaxM) {
-        const FewShape f = few_shape(M, N, gated);
-        int fit = 160 * 1024 / (kFewWaves * (f.rb + f.cb) * 2048 * few_slots(f.rb, f.cb));
-        if (fit > 3) fit = 3;
-        double rounds = fit == 1 ? (double)cdiv(f.workgroups, 256) : (double)f.workgroups / 256.0;
-        if (rounds < 1.0) rounds = 1.0;
-        if (floored(2.0 + rounds * (2.0 / fit + 16.0 * (f.rb + f.cb) * kbytes / 85e3)) <= least) best = C_FEW;
+        if (t < least) least = t, best = Choice{(ShapeClass)(C_128x128 + c), {}};
     }
     return best;
 }
@@ -210,11 +219,12 @@ int launch_few_rb(const FusedArgs &a, const FewShape &f, hipStream_t s) {
 }
 
 template <int FA, int FB, int EPI>
-int launch_few_fmt(const FusedArgs &a, hipStream_t s) {
-    constexpr int R0 = EPI == fp8g::EPI_GATED ? 2 : 1;
-    const FewShape f = few_shape(a.M, a.N, EPI == fp8g::EPI_GATED);
-    if (f.rb == R0) return launch_few_rb<R0, FA, FB, EPI>(a, f, s);
-    return launch_few_rb<2 * R0, FA, FB, EPI>(a, f, s);
+int launch_few_fmt(const FusedArgs &a, const FewShape &f, hipStream_t s) {
+    if constexpr (EPI != fp8g::EPI_GATED) {
+        if (f.rb == 1) return launch_few_rb<1, FA, FB, EPI>(a, f, s);
+    }
+    if (f.rb == 2) return launch_few_rb<2, FA, FB, EPI>(a, f, s);
+    return launch_few_rb<4, FA, FB, EPI>(a, f, s);
 }
 
 }  // namespace

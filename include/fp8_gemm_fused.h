@@ -56,7 +56,7 @@ typedef enum {
  *   R: [M][ldr] BF16 or NULL = 0.  R may be D itself, with ldr = ldd.
  * The kernel is chosen by an estimate of its time (fp8_gemm_fused_plan): for
  * few tokens or few output columns the swapped decode kernel (4 waves
- * splitting K over 16 or 32 weight rows, tokens in tiles of up to 64), else
+ * splitting K over 16, 32 or 64 weight rows, tokens in tiles of up to 64), else
  * the LDS-tiled one with 128 x 128, 128 x 256 or 256 x 256 tiles.  The choice
  * never changes which elements are written.
  */

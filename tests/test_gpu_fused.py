@@ -166,17 +166,25 @@ def test_gated_bf16_backward(f, M, N, K, name):
     F.check(gu, *F.backward_products(du.t(), err_u.t(), a), M, f"grad_up {name}")
 
 
-# Every class of the tiled kernels with ragged edges, by the plan: (op, M, N, K) with few K so that the 64-bit
-# reference stays small.
-CLASS_CASES = [(0, 4000, 3000, 144, 1), (0, 2000, 2050, 272, 2), (0, 700, 1300, 272, 7), (0, 300, 70, 272, 4),
-               (1, 3000, 2100, 144, 1), (1, 2000, 1025, 272, 2), (1, 500, 1300, 272, 7), (1, 200, 70, 272, 4),
-               (2, 4000, 3000, 136, 1), (2, 2000, 2050, 200, 2), (2, 700, 1300, 200, 7), (2, 300, 70, 200, 4),
-               (3, 3000, 2100, 136, 1), (3, 2000, 1025, 200, 2), (3, 500, 1300, 200, 7), (3, 200, 70, 200, 4)]
+# Every class of the kernels with ragged edges, by the plan (variant; the few-token kernel's weight rows and 16-token
+# blocks): (op, M, N, K), with a short K so that the 64-bit reference stays small.
+CLASS_CASES = [
+    (0, 4000, 2050, 272, 1, 0, 0), (0, 130, 17001, 272, 2, 0, 0), (0, 2050, 77, 272, 7, 0, 0), (0, 1, 77, 272, 4, 16, 1),
+    (0, 20, 77, 272, 4, 16, 2), (0, 40, 77, 272, 4, 16, 4), (0, 1, 5003, 272, 4, 32, 1), (0, 20, 9003, 272, 4, 32, 2),
+    (0, 130, 2503, 272, 4, 32, 4), (0, 1, 17003, 272, 4, 64, 1), (0, 32, 14339, 4096, 4, 64, 2), (0, 40, 9001, 272, 4, 64, 4),
+    (1, 130, 17001, 272, 1, 0, 0), (1, 130, 9001, 272, 2, 0, 0), (1, 2050, 77, 272, 7, 0, 0), (1, 1, 77, 272, 4, 16, 1),
+    (1, 20, 77, 272, 4, 16, 2), (1, 40, 77, 272, 4, 16, 4), (1, 1, 9003, 272, 4, 32, 1), (1, 40, 4101, 272, 4, 32, 4),
+    (2, 4000, 2050, 200, 1, 0, 0), (2, 130, 17001, 200, 2, 0, 0), (2, 2050, 77, 200, 7, 0, 0), (2, 1, 77, 200, 4, 16, 1),
+    (2, 20, 77, 200, 4, 16, 2), (2, 40, 77, 200, 4, 16, 4), (2, 1, 5003, 200, 4, 32, 1), (2, 20, 9003, 200, 4, 32, 2),
+    (2, 130, 2503, 200, 4, 32, 4), (2, 1, 17003, 200, 4, 64, 1), (2, 40, 9001, 200, 4, 64, 4),
+    (3, 130, 17001, 200, 1, 0, 0), (3, 130, 9001, 200, 2, 0, 0), (3, 2050, 77, 200, 7, 0, 0), (3, 1, 77, 200, 4, 16, 1),
+    (3, 20, 77, 200, 4, 16, 2), (3, 40, 77, 200, 4, 16, 4), (3, 1, 9003, 200, 4, 32, 1), (3, 40, 4101, 200, 4, 32, 4)]
 
 
-@pytest.mark.parametrize("op,M,N,K,variant", CLASS_CASES)
-def test_every_class(f, op, M, N, K, variant):
-    assert f.fused_plan(op, M, N, K).variant == variant
+@pytest.mark.parametrize("op,M,N,K,variant,rows,blocks", CLASS_CASES)
+def test_every_class(f, op, M, N, K, variant, rows, blocks):
+    p = f.fused_plan(op, M, N, K)
+    assert p.variant == variant and (variant != 4 or (p.tile_n, p.token_blocks) == (rows, blocks))
     dt = E4 if op < 2 else BF
     a, b = rand(1, M, K, dtype=dt), rand(2, N, K, dtype=dt, std=0.25)
     if op in (0, 2):

@@ -158,8 +158,8 @@ def test_backward_splits(f, m, n, k, splits):
 
 
 @pytest.mark.parametrize("op,m,n,k,variant", [
-    (0, 1, 4096, 4096, 4), (0, 64, 4096, 14336, 4), (0, 512, 4096, 4096, 7), (0, 2048, 4096, 4096, 2), (0, 4096, 4096, 4096, 1),
-    (1, 1, 14336, 4096, 4), (1, 64, 14336, 4096, 7), (1, 8192, 14336, 4096, 1), (2, 16, 4096, 2048, 4), (3, 4096, 14336, 4096, 1),
+    (0, 1, 4096, 4096, 4), (0, 64, 4096, 14336, 4), (0, 512, 4096, 4096, 4), (0, 2049, 512, 512, 7), (0, 2048, 4096, 4096, 2), (0, 4096, 4096, 4096, 1),
+    (1, 1, 14336, 4096, 4), (1, 64, 14336, 4096, 4), (1, 256, 14336, 4096, 2), (1, 8192, 14336, 4096, 1), (2, 16, 4096, 2048, 4), (3, 4096, 14336, 4096, 1),
     (4, 4096, 4096, 28672, 1), (4, 1, 64, 64, 7), (0, 0, 5, 16, 0), (4, 5, 0, 3, 0),
 ])
 def test_plan(f, op, m, n, k, variant):
