@@ -700,13 +700,17 @@ def gated_nt(a, w_gate, w_up, scale_a=None, scale_gate=None, scale_up=None, acti
 
 
 def _gated_preact(tt, preact, M, N):
-    """(gate, up, row stride) pointers of a float32 [2, M, N] tensor."""
+    """(gate, up, row stride) pointers of a float32 [2, M, N] tensor, whose two matrices do not overlap (one
+    behind the other, or their rows in turn)."""
     if preact.dim() != 3 or preact.shape[0] != 2:
         raise ValueError(f"preact must be a [2, {M}, {N}] tensor, got {list(preact.shape)}")
     gate = preact[0]
     ld = _rows(gate, "preact", M, N, tt.f32)
+    step = preact.stride(0)
+    if M and N and step < (M - 1) * ld + N and (step < N or ld < step + N):
+        raise ValueError("preact: its two matrices overlap")
     pointer = gate.data_ptr()
-    return pointer, pointer + 4 * preact.stride(0), ld
+    return pointer, pointer + 4 * step, ld
 
 
 def gated_nt_bf16(a, w_gate, w_up, activation="silu", out=None, preact=None):

@@ -237,15 +237,14 @@ __device__ __forceinline__ void stage_f32(uint8_t *smem, int s, int col, v4f v) 
 
 // Copies the tile's terms into LDS: floats [0, 256) row scales, [256, 512)
 // column scales (gated: [256, 384) the first matrix's, [384, 512) the
-// second's), [512, 768) biases, 64 of each per wave of the first four, one
-// dword per lane, asynchronously (the wait for the ring's step 0 covers them).
-// Entries past the tile's rows or columns read as zeros; absent scales are
-// ones, absent biases zeros.
+// second's), [512, 768) biases, 64 of each per wave, one dword per lane,
+// asynchronously (the wait for the ring's step 0 covers them).  Entries past
+// the tile's rows or columns read as zeros; absent scales are ones, absent
+// biases zeros.
 template <class P>
 __device__ __forceinline__ void copy_tile_terms(const P &p, uint8_t *terms, uint32_t lds, int wave, int lane, int m0,
                                                 int rows_m, int n0, int rows_n) {
     constexpr bool GATED = P::kEpilogue == EPI_GATED;
-    if (wave >= 4) return;
     float *const own = reinterpret_cast<float *>(terms) + wave * 64 + lane;
     auto copy = [&](const float *src, int step, int first, int count, int idx, int at, float absent) {
         if (src)
@@ -263,14 +262,14 @@ __device__ __forceinline__ void copy_tile_terms(const P &p, uint8_t *terms, uint
     if (P::kEpilogue == EPI_ACT) copy(p.bias, 1, n0, rows_n, idx, 512, 0.0f);
 }
 
-template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf, class Stage>
+template <int BN, int ROWS, class P, class RowOf, class Stage>
 __device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, const uint8_t *terms, int tid, int m0,
                                                  int rows_m, int n0, uint16_t *d, RowOf row_of, Stage stage) {
     constexpr int EPI = P::kEpilogue;
     constexpr bool GATED = EPI == EPI_GATED;
-    constexpr int GROUPS = (GATED ? BN / 2 : BN) / 8, RPI = THREADS / GROUPS, NIT = ROWS / RPI;
-    // (8 waves per workgroup have half the registers each)
-    constexpr int U = THREADS == 256 ? 4 : GATED ? 1 : 2;
+    constexpr int THREADS = 256, GROUPS = (GATED ? BN / 2 : BN) / 8, RPI = THREADS / GROUPS, NIT = ROWS / RPI;
+    constexpr int U = 4;                           // rows per batch
+    constexpr int IB = 16;                         // gated: columns of a block of one matrix
     static_assert(THREADS % GROUPS == 0 && ROWS % RPI == 0 && NIT % U == 0, "rows split evenly over the threads");
     const int g = tid % GROUPS;
     const int n = n0 + 8 * g;
@@ -290,8 +289,8 @@ __device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem
     if constexpr (EPI == EPI_ACT) load_residuals(rb[0], 0);
     stage();
     if (nv <= 0) return;
-    // first 16-byte chunk of the group's sums (gated: blocks of IB columns of
-    // the two matrices alternate)
+    // first 16-byte chunk of the group's sums (gated: the two matrices' blocks
+    // alternate)
     const uint32_t c0 = GATED ? (uint32_t)((g / (IB / 8)) * (IB / 2) + (g % (IB / 8)) * 2) : (uint32_t)(2 * g);
     auto read8 = [&](int s, uint32_t c, float (&z)[8]) {
         const uint8_t *row = smem + s * (BN * 4);
@@ -381,9 +380,10 @@ __global__ __launch_bounds__(256, 1) void fused_tile16_kernel(FusedParams<EPI, t
     tile16_body<BM, BN, STAGES, FA, FB, MODE_DENSE, SCALE_CHANNEL, KTAIL>(p);
 }
 
-// Few tokens, FP8 and BF16.
-template <int WAVES, int RB, int CB, int FA, int FB, int D, int EPI, int OCC>
-__global__ __launch_bounds__(64 * WAVES, OCC) void fused_decode_kernel(FusedParams<EPI, FA != FMT_BF16> p) {
+// Few tokens, FP8 and BF16.  (Builds for one workgroup per CU, as the dense
+// form has for grids of up to 256, measured within 1% of these for two.)
+template <int WAVES, int RB, int CB, int FA, int FB, int D, int EPI>
+__global__ __launch_bounds__(64 * WAVES, 2) void fused_decode_kernel(FusedParams<EPI, FA != FMT_BF16> p) {
     decode_body<WAVES, RB, CB, FA, FB, D, SCALE_CHANNEL>(p);
 }
 

@@ -218,6 +218,7 @@ int bf16_gated_nt(const void *A, int64_t lda, const void *Wg, int64_t ldg, const
     if (!pre_g != !pre_u) return fail(FP8G_ERR_NULL, "pre_g and pre_u are given together or not at all");
     if (pre_g && ((st = check_rows("pre_g", pre_g, ldp, N, 4, &p_vec)) || (st = check_rows("pre_u", pre_u, ldp, N, 4, &p_vec2))))
         return st;
+    if (pre_g && pre_g == pre_u) return fail(FP8G_ERR_ARG, "pre_g and pre_u are the same matrix");
     if ((st = check_device())) return st;
     FusedArgs p = base_args(A, lda, Wg, ldg, D, ldd, M, N, K);
     p.B2 = static_cast<const uint8_t *>(Wu);
@@ -257,6 +258,7 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
     if (want_w && ((M > 0 && (st = check_operand("A", A, lda, K, 2))) || (st = check_output("dWg", dWg, lddw, K)) ||
                    (st = check_output("dWu", dWu, lddw, K))))
         return st;
+    if (want_w && dWg == dWu) return fail(FP8G_ERR_ARG, "dWg and dWu are the same matrix");
     if ((st = check_device())) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t cols = pad64(N);

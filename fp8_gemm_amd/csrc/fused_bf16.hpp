@@ -290,7 +290,7 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
     };
 #pragma unroll 1
     for (int h = 0; h < FPASS; ++h)
-        fused_store_rows<BN, WM * RW, THREADS, 16>(
+        fused_store_rows<BN, WM * RW>(
             p, smem, smem + RING, tid, m0, rows_m, n0, d, [=](int s) { return (s / RW) * TM + h * RW + s % RW; },
             [&] {
                 if (h == 0) {
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams p) {
             load_bf16_row<8>(p.G + (int64_t)r * p.ldg + n, nv, p.g_vec, g);
             if (GATED || act.value != ACT_NONE) load_f32_row8(p.pre + (int64_t)r * p.ldp + n, nv, p.p_vec, z);
             if (GATED) load_f32_row8(p.pre2 + (int64_t)r * p.ldp + n, nv, p.p_vec, z2);
-    #pragma unroll
+#pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (e >= nv) {                         // (a padding column is zero whatever its gradient)
                     dz[e] = du[e] = 0.0f;

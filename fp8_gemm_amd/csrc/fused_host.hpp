@@ -203,11 +203,7 @@ int launch_few(const FusedArgs &a, int64_t workgroups, hipStream_t s) {
     const auto p = with_epilogue<EPI, FA != fp8g::FMT_BF16>(a);
     const unsigned tiles = (unsigned)cdiv(p.M, 64);
     const dim3 grid((unsigned)(workgroups / tiles), tiles), block(64 * kFewWaves);
-    constexpr int D = few_slots(RB, CB);
-    if (workgroups <= 256)
-        hipLaunchKernelGGL((fp8g::fused_decode_kernel<kFewWaves, RB, CB, FA, FB, D, EPI, 1>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((fp8g::fused_decode_kernel<kFewWaves, RB, CB, FA, FB, D, EPI, 2>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((fp8g::fused_decode_kernel<kFewWaves, RB, CB, FA, FB, few_slots(RB, CB), EPI>), grid, block, 0, s, p);
     return launch_status("fused few-token kernel");
 }
 

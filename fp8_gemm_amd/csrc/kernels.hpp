@@ -90,7 +90,7 @@ struct int_c {
 };
 template <int BN>
 __device__ __forceinline__ void stage_f32(uint8_t *smem, int s, int col, v4f v);
-template <int BN, int ROWS, int THREADS, int IB, class P, class RowOf, class Stage>
+template <int BN, int ROWS, class P, class RowOf, class Stage>
 __device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem, const uint8_t *terms, int tid, int m0,
                                                  int rows_m, int n0, uint16_t *d, RowOf row_of, Stage stage);
 template <class P>
@@ -1210,7 +1210,7 @@ __device__ __forceinline__ void tile16_body(P p) {
         // out of the instruction cache)
 #pragma unroll 1
         for (int h = 0; h < FPASS; ++h)
-            fused_store_rows<BN, WM * RW, THREADS, 16>(
+            fused_store_rows<BN, WM * RW>(
                 p, smem, smem + CH_AT, (int)threadIdx.x, m0, rows_m, n0, p.D,
                 [=](int s) { return (s / RW) * TM + h * RW + s % RW; },
                 [&] {
@@ -1255,12 +1255,11 @@ __device__ __forceinline__ void tile16_body(P p) {
             __builtin_amdgcn_sched_barrier(0);     // one token block at a time: bounded live registers
         }
     }
-    if constexpr (EPI != EPI_STORE) {
-    } else if constexpr (!BLK) {
+    if constexpr (EPI == EPI_STORE && !BLK) {
         __syncthreads();
         const int etid = PASSES > 1 ? wave * 64 + el : tid;   // formed afresh, as above
         store_staged<BM, BN, THREADS, MODE>(p, smem, etid, spot, p.D, rowmask);
-    } else {
+    } else if constexpr (BLK) {
         // Block scales: each wave stages its own TM x TN outputs in a private
         // part of the (now free) ring, in its token-block order (row r =
         // 16 i + c at r * TN * 2 bytes, chunk at stage_chunk<WCH>(c, r)), and

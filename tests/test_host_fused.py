@@ -221,3 +221,29 @@ def test_wrapper_refusals(f):
         f._gated_preact(f._tt(), torch.zeros(4, 8), 4, 8)
     with pytest.raises(ValueError, match="1"):
         f._floats(f._tt(), torch.zeros(3), "scale_a", 4)
+
+
+@pytest.mark.parametrize("M,N,strides,overlap", [
+    (4, 8, (32, 8, 1), False), (4, 8, (8, 16, 1), False), (4, 8, (28, 8, 1), True), (4, 8, (0, 8, 1), True),
+    (4, 8, (4, 16, 1), True), (4, 8, (8, 12, 1), True), (1, 8, (8, 8, 1), False), (1, 8, (7, 8, 1), True),
+    (0, 8, (0, 8, 1), False), (4, 5, (8, 16, 1), False),
+])
+def test_preact_matrices_overlap(f, M, N, strides, overlap):
+    t = torch.zeros(256).as_strided((2, M, N), strides)
+    assert overlap == (len(set((r * strides[1] + p * strides[0] + c) for p in range(2) for r in range(M)
+                               for c in range(N))) < 2 * M * N)
+    if overlap:
+        with pytest.raises(ValueError, match="overlap"):
+            f._gated_preact(f._tt(), t, M, N)
+    else:
+        gate, up, ld = f._gated_preact(f._tt(), t, M, N)
+        assert up - gate == 4 * strides[0] and ld == (strides[1] if M > 1 else N)
+
+
+def test_same_matrix_twice(f):
+    lib = f.load_library()
+    st = lib.bf16_gated_nt(A16, 64, A16, 64, A16, 64, 2, A16, 64, A256, A256, 64, 64, 64, 64, None)
+    assert st == -8 and "pre_g and pre_u" in lib.fp8_gemm_strerror(st).decode()
+    st = lib.bf16_gated_nt_backward(A16, 64, A16, 64, A16, 64, A16, 64, A16, A16, 64, 2, A16, 64, A256, A256, 64, A256,
+                                    1 << 40, 64, 64, 64, None)
+    assert st == -8 and "dWg and dWu" in lib.fp8_gemm_strerror(st).decode()
