@@ -338,7 +338,7 @@ __device__ __forceinline__ float act_value_exact(float z) {
 // act'(G) and dU = dH act(G), rounded to BF16 once, the operands of the
 // backward products, into W [M][ldw] (gated: dU from column ldw / 2 on), whose
 // columns past N hold zeros.  Bound by memory: 6 bytes read and 2 written per
-// element (fused), 10 and 4 (gated).
+// element (fused), 10 and 4 (gated); gated 4096 x 14336 188 us, 4.4 TB/s.
 // BIAS: also the column sums of the FP32 dZ over the block's rows into
 // part[block row][N], added over the rows in a fixed order.
 // A block is 32 groups of 8 columns x 8 rows of threads over `rows` rows: as
