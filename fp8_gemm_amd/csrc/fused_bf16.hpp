@@ -303,11 +303,16 @@ __global__ __launch_bounds__(256, 1) void bf16_tile_kernel(FusedParams<EPI, fals
             });
 }
 
-// act'(z).  Beyond |z| = 30 every activation here has its limit slope to FP32
-// precision; the clamp keeps z^2 and z^3 finite (0 times infinity).
+// act'(z), for z within a range outside of which act' has its limit value in
+// FP32; the clamp keeps z, z^2 and z^3 finite (0 times infinity).  Above 30
+// that holds for every activation here, below -30 for both forms of GELU
+// (their slopes fall faster than exp(-z^2 / 2 + log |z|)); the slope of SiLU
+// falls like |z| exp(z) only, down to the FP32 exponential's overflow at z =
+// -88.7, past which the sigmoid, and with it the slope, is 0.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z0) {
-    const float z = z0 > 30.0f ? 30.0f : (z0 < -30.0f ? -30.0f : z0);
+    constexpr float lo = ACT == ACT_SILU ? -100.0f : -30.0f;
+    const float z = z0 > 30.0f ? 30.0f : (z0 < lo ? lo : z0);
     if constexpr (ACT == ACT_RELU) {
         return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     } else if constexpr (ACT == ACT_SILU) {
