@@ -56,9 +56,11 @@ struct FusedParams : FusedArgs {
 
 // ---------------------------------------------------------------------------
 // Activations, in FP32.  x sigmoid(v) is x / (1 + exp(-v)): no cancellation at
-// either end (exp overflows to infinity for v < -88, and the quotient is then
-// -0).  The tanh form of GELU is x sigmoid(2 u), since (1 + tanh u) / 2 =
-// sigmoid(2 u).
+// either end.  The reciprocal instruction returns 0 for results below 2^-126,
+// so it is taken of (1 + exp(-v)) / 4, which stays in its range up to the
+// exponential's overflow at -v = 88.7 (silu(-88) = -5.3e-37 is a normal BF16
+// number); past that the quotient is -0.  The tanh form of GELU is
+// x sigmoid(2 u), since (1 + tanh u) / 2 = sigmoid(2 u).
 // The exact form is x Phi(x), Phi the normal distribution: x Q for x < 0 and
 // x (1 - Q) otherwise, with Q = Phi(-|x|) = exp(-x^2 / 2) h(|x|), which keeps
 // its relative precision where 1 + erf would cancel.  h(x) = erfcx(x / sqrt 2)
@@ -74,7 +76,7 @@ constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
 __device__ __forceinline__ float sigmoid_times(float x, float v) {
-    return x * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+    return (0.25f * x) * __builtin_amdgcn_rcpf(0.25f + 0.25f * __expf(-v));
 }
 
 __device__ __forceinline__ float normal_cdf(float z) {

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import _fused as F
-from tests.test_gpu_fused import BF, DEV, f  # noqa: F401 (f: fixture)
+from tests.test_gpu_fused import BF, DEV, E4, f  # noqa: F401 (f: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,27 @@ def test_slopes_far_from_zero(f, name, points):
         tol = tol + torch.where(z64 < -OVERFLOW, 2.0 ** -128 * z64.abs().clamp(max=128), torch.zeros_like(z64))
     off = (got - want).abs()
     assert (off <= tol).all(), [(p, g, w) for p, g, w, bad in zip(points, got.tolist(), want.tolist(), off > tol) if bad]
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 100, 2100])
+def test_small_sigmoids(f, name, M):
+    """Sigmoids between 2^-128 and 2^-126, whose products with z are normal BF16 numbers."""
+    v = torch.tensor([-87.0, -87.2, -87.4, -87.7, -88.0, -88.3, -88.6], dtype=torch.float64)
+    z = v if name == "silu" else torch.linspace(-10.06, -9.98, 81, dtype=torch.float64)
+    z = z.float().repeat(300)[:300]
+    z64 = z.double()
+    if name == "gelu_tanh":
+        z64 = z64[exponent(name, z64) > -OVERFLOW]
+        assert (exponent(name, z64) < -87.4).any()
+    n = len(z64)
+    bias = z64.float().to(DEV)
+    want, _ = F.act(name, z64)
+    # one rounding, and FP32: up to eight roundings of 2^-24 in the exponent's argument (the tanh form's polynomial, its
+    # two constants, the factor log2 e), which is at most 89: 8 * 89 * 2^-24 < 2^-14
+    tol = (F.EPS + 2.0 ** -14) * want.abs()
+    x, w = torch.zeros(M, 16, device=DEV), torch.zeros(n, 16, device=DEV)
+    for got in (f.gemm_nt_bf16_fused(x.to(BF), w.to(BF), bias=bias, activation=name),
+                f.gemm_nt_fused(x.to(E4), w.to(E4), bias=bias, activation=name)):
+        off = (got.cpu().double() - want).abs()
+        assert (off <= tol).all(), (float(z64[(off > tol).any(0)][0]), int((off > tol).sum()))
