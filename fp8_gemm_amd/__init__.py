@@ -582,7 +582,9 @@ def gemm_nt_fused(a, b, scale_a=None, scale_b=None, bias=None, activation="none"
     scale_a: float32, M elements or 1, or None (1); scale_b: float32, N elements
     or 1, or None; bias: float32 [N] or None; activation: "none", "relu",
     "silu", "gelu" (erf) or "gelu_tanh"; residual: bfloat16 [M, N] with any row
-    stride, or None; it may be `out` itself.
+    stride, or None; it may be `out` itself.  Otherwise `out` must not share
+    memory with an operand (columns of one buffer that do not overlap may be
+    both); the library refuses such calls.
     """
     tt = _tt()
     fa, fb = _fp8_of(tt, a, a_dtype, "a"), _fp8_of(tt, b, b_dtype, "b")
@@ -606,7 +608,8 @@ def gemm_nt_bf16_fused(a, b, bias=None, activation="none", residual=None, out=No
         z = a[m] . b[n] + bias[n];  out[M, N] = bf16(act(z) + residual[m, n])
 
     Arguments as for gemm_nt_fused.  preact: a float32 [M, N] tensor that
-    receives z, for gemm_nt_bf16_fused_backward, or None.
+    receives z, for gemm_nt_bf16_fused_backward, or None; it is an output, and
+    must not share memory with another one or an operand.
     """
     tt = _tt()
     _bf16_only(tt, a=a, b=b)

@@ -133,7 +133,11 @@ int bf16_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, c
         return st;
     if (R && (st = check_rows("R", R, ldr, N, 2, &r_vec))) return st;
     if (preact && (st = check_rows("preact", preact, ldp, N, 4, &p_vec))) return st;
-    if ((st = check_device())) return st;
+    if ((st = check_apart({area("D", D, ldd, M, N, 2), area("preact", preact, ldp, M, N, 4)},
+                          {area("A", A, lda, M, K, 2), area("B", B, ldb, N, K, 2), area("bias", bias, N, 4),
+                           residual_area(R, ldr, D, ldd, M, N)})) ||
+        (st = check_device()))
+        return st;
     FusedArgs p = base_args(A, lda, B, ldb, D, ldd, M, N, K);
     p.bias = bias;
     p.act = activation;
@@ -165,7 +169,15 @@ int bf16_gemm_nt_fused_backward(const void *G, int64_t ldg, const void *A, int64
     const bool want_a = dA && M > 0 && K > 0, want_b = dB && N > 0 && K > 0;
     if (want_a && ((N > 0 && (st = check_operand("B", B, ldb, K, 2))) || (st = check_output("dA", dA, ldda, K)))) return st;
     if (want_b && ((M > 0 && (st = check_operand("A", A, lda, K, 2))) || (st = check_output("dB", dB, lddb, K)))) return st;
-    if ((st = check_floats("dbias", dbias)) || (st = check_device())) return st;
+    if ((st = check_floats("dbias", dbias)) ||
+        (st = check_apart({area("dA", want_a ? dA : nullptr, ldda, M, K, 2), area("dB", want_b ? dB : nullptr, lddb, N, K, 2),
+                           area("dbias", dbias, N, 4),
+                           area("workspace", workspace, M > 0 && N > 0 ? bf16_gemm_nt_fused_backward_workspace(M, N, K) : 0, 1)},
+                          {area("G", G, ldg, M, N, 2), area("A", A, lda, want_b ? M : 0, K, 2),
+                           area("B", B, ldb, want_a ? N : 0, K, 2),
+                           area("preact", activation != FP8G_ACT_NONE ? preact : nullptr, ldp, M, N, 4)})) ||
+        (st = check_device()))
+        return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
 
     // dZ: G itself where there is no activation and its rows are whole chunks,
@@ -218,8 +230,10 @@ int bf16_gated_nt(const void *A, int64_t lda, const void *Wg, int64_t ldg, const
     if (!pre_g != !pre_u) return fail(FP8G_ERR_NULL, "pre_g and pre_u are given together or not at all");
     if (pre_g && ((st = check_rows("pre_g", pre_g, ldp, N, 4, &p_vec)) || (st = check_rows("pre_u", pre_u, ldp, N, 4, &p_vec2))))
         return st;
-    if (pre_g && pre_g == pre_u) return fail(FP8G_ERR_ARG, "pre_g and pre_u are the same matrix");
-    if ((st = check_device())) return st;
+    if ((st = check_apart({area("pre_g", pre_g, ldp, M, N, 4), area("pre_u", pre_u, ldp, M, N, 4), area("D", D, ldd, M, N, 2)},
+                          {area("A", A, lda, M, K, 2), area("Wg", Wg, ldg, N, K, 2), area("Wu", Wu, ldu, N, K, 2)})) ||
+        (st = check_device()))
+        return st;
     FusedArgs p = base_args(A, lda, Wg, ldg, D, ldd, M, N, K);
     p.B2 = static_cast<const uint8_t *>(Wu);
     p.ldb2 = 2 * ldu;
@@ -258,8 +272,14 @@ int bf16_gated_nt_backward(const void *G, int64_t ldgrad, const void *A, int64_t
     if (want_w && ((M > 0 && (st = check_operand("A", A, lda, K, 2))) || (st = check_output("dWg", dWg, lddw, K)) ||
                    (st = check_output("dWu", dWu, lddw, K))))
         return st;
-    if (want_w && dWg == dWu) return fail(FP8G_ERR_ARG, "dWg and dWu are the same matrix");
-    if ((st = check_device())) return st;
+    if ((st = check_apart({area("dWg", want_w ? dWg : nullptr, lddw, N, K, 2), area("dWu", want_w ? dWu : nullptr, lddw, N, K, 2),
+                           area("dA", want_a ? dA : nullptr, ldda, M, K, 2),
+                           area("workspace", workspace, M > 0 && N > 0 ? bf16_gated_nt_backward_workspace(M, N, K) : 0, 1)},
+                          {area("G", G, ldgrad, M, N, 2), area("A", A, lda, want_w ? M : 0, K, 2),
+                           area("Wg", Wg, ldg, want_a ? N : 0, K, 2), area("Wu", Wu, ldu, want_a ? N : 0, K, 2),
+                           area("pre_g", pre_g, ldp, M, N, 4), area("pre_u", pre_u, ldp, M, N, 4)})) ||
+        (st = check_device()))
+        return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t cols = pad64(N);
     uint16_t *const w = static_cast<uint16_t *>(workspace);

@@ -93,7 +93,12 @@ int fp8_gemm_nt_fused(const void *A, int64_t lda, int a_dtype, const void *B, in
         (st = check_scale("scale_b", scale_b, scale_b_n, N, &p.sb_step)) || (st = check_floats("bias", bias)))
         return st;
     if (R && (st = check_rows("R", R, ldr, N, 2, &p.r_vec))) return st;
-    if ((st = check_device())) return st;
+    if ((st = check_apart({area("D", D, ldd, M, N, 2)},
+                          {area("A", A, lda, M, K, 1), area("B", B, ldb, N, K, 1), residual_area(R, ldr, D, ldd, M, N),
+                           area("scale_a", scale_a, scale_a_n, 4), area("scale_b", scale_b, scale_b_n, 4),
+                           area("bias", bias, N, 4)})) ||
+        (st = check_device()))
+        return st;
     p.A = static_cast<const uint8_t *>(A);
     p.B = static_cast<const uint8_t *>(B);
     p.D = static_cast<uint16_t *>(D);
@@ -119,7 +124,12 @@ int fp8_gated_nt(const void *A, int64_t lda, int a_dtype, const void *Wg, int64_
         (st = check_scale("scale_g", scale_g, scale_w_n, N, &p.sb_step)) ||
         (st = check_scale("scale_u", scale_u, scale_w_n, N, &step_u)))
         return st;
-    if ((st = check_device())) return st;
+    if ((st = check_apart({area("D", D, ldd, M, N, 2)},
+                          {area("A", A, lda, M, K, 1), area("Wg", Wg, ldg, N, K, 1), area("Wu", Wu, ldu, N, K, 1),
+                           area("scale_a", scale_a, scale_a_n, 4), area("scale_g", scale_g, scale_w_n, 4),
+                           area("scale_u", scale_u, scale_w_n, 4)})) ||
+        (st = check_device()))
+        return st;
     p.A = static_cast<const uint8_t *>(A);
     p.B = static_cast<const uint8_t *>(Wg);
     p.B2 = static_cast<const uint8_t *>(Wu);

@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "../../include/fp8_gemm_fused.h"
 #include "fused.hpp"
 #include "host_common.hpp"
@@ -75,6 +77,59 @@ int check_scale(const char *name, const float *ptr, int n, int rows, int *step) 
     if (n != rows && n != 1) return fail(FP8G_ERR_ARG, "%s has %d values: 1 or %d are wanted", name, n, rows);
     *step = n == rows && rows != 1;
     return check_floats(name, ptr);
+}
+
+// A matrix in memory: rows of `width` bytes, `ld` bytes apart (ld >= width).
+struct Area {
+    const char *name;
+    const void *ptr;
+    int64_t ld, rows, width;
+};
+
+Area area(const char *name, const void *ptr, int64_t ld, int64_t rows, int64_t cols, int unit) {
+    return Area{name, ptr, ld * unit, ptr ? rows : 0, cols * unit};
+}
+Area area(const char *name, const void *ptr, int64_t count, int unit) { return area(name, ptr, count, 1, count, unit); }
+
+// Whether two matrices share a byte (rows of one may lie between rows of the
+// other).  Rows are gone through one by one only where the strides differ and
+// the spans of memory meet.
+bool share(const Area &x, const Area &y) {
+    if (x.rows <= 0 || y.rows <= 0 || x.width <= 0 || y.width <= 0) return false;
+    const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(x.ptr), b = (int64_t)reinterpret_cast<uintptr_t>(y.ptr);
+    if (a >= b + (y.rows - 1) * y.ld + y.width || b >= a + (x.rows - 1) * x.ld + x.width) return false;
+    auto floor_div = [](int64_t n, int64_t d) { return n / d - (n % d < 0); };
+    // whether -before < gap + t ld < after for some t in lo .. hi
+    auto meets = [&](int64_t gap, int64_t ld, int64_t before, int64_t after, int64_t lo, int64_t hi) {
+        const int64_t first = -floor_div(before - 1 + gap, ld), last = floor_div(after - 1 - gap, ld);
+        return (first > lo ? first : lo) <= (last < hi ? last : hi);
+    };
+    // (t: row of y less row of x)
+    if (x.ld == y.ld) return meets(b - a, x.ld, y.width, x.width, 1 - x.rows, y.rows - 1);
+    const bool swap = x.rows > y.rows;
+    const Area &few = swap ? y : x, &many = swap ? x : y;
+    const int64_t gap = swap ? a - b : b - a;
+    for (int64_t i = 0; i < few.rows; ++i)
+        if (meets(gap - i * few.ld, many.ld, many.width, few.width, 0, many.rows - 1)) return true;
+    return false;
+}
+
+// No output may share memory with another output or an operand: tiles are
+// written while others are still being read.
+int check_apart(std::initializer_list<Area> outputs, std::initializer_list<Area> operands) {
+    for (const Area *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Area *q = o + 1; q != outputs.end(); ++q)
+            if (share(*o, *q)) return fail(FP8G_ERR_ARG, "%s and %s overlap", o->name, q->name);
+        for (const Area &q : operands)
+            if (share(*o, q)) return fail(FP8G_ERR_ARG, "%s overlaps %s", o->name, q.name);
+    }
+    return FP8G_OK;
+}
+
+// The residual of an output: another matrix, or the output itself.
+Area residual_area(const void *R, int64_t ldr, const void *D, int64_t ldd, int M, int N) {
+    const bool same = R == D && (ldr == ldd || M == 1);
+    return area("R", same ? nullptr : R, ldr, M, N, 2);
 }
 
 // ---------------------------------------------------------------------------

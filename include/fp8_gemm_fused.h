@@ -19,6 +19,10 @@
  *   - Residuals, output gradients and pre-activations may have any row stride
  *     >= N and any alignment of their element type; rows that start 16-byte
  *     aligned are read and written in 16-byte accesses.
+ *   - An output (and the workspace) must not share memory with another output
+ *     or an operand: such calls are refused with FP8G_ERR_ARG.  Rows of one may
+ *     lie between rows of the other (column ranges of one buffer), operands
+ *     may overlap each other, and the residual may be the output itself.
  *   - K = 0 gives Z = bias; M = 0 gives zero weight and bias gradients.
  *
  * Activations: z; max(z, 0); z / (1 + exp(-z)); z (1 + erf(z / sqrt 2)) / 2;
@@ -53,7 +57,8 @@ typedef enum {
  *     scale_b_n floats, scale_b_n = N (one per output channel) or 1; either
  *     pointer NULL = 1.
  *   bias: [N] floats or NULL = 0.  Scales and bias 4-byte aligned.
- *   R: [M][ldr] BF16 or NULL = 0.  R may be D itself, with ldr = ldd.
+ *   R: [M][ldr] BF16 or NULL = 0.  R may be D itself, with ldr = ldd; a matrix
+ *     that overlaps D in another way is refused.
  * The kernel is chosen by an estimate of its time (fp8_gemm_fused_plan): for
  * few tokens or few output columns the swapped decode kernel (4 waves
  * splitting K over 16, 32 or 64 weight rows, tokens in tiles of up to 64), else
