@@ -54,8 +54,11 @@ __device__ __forceinline__ v4i make_srd(const void *base, uint32_t bytes) {
 // reading the data.  Written as inline assembly so the compiler does not
 // insert its own conservative vmcnt(0) before every LDS read; the "memory"
 // clobber keeps other memory operations from moving across it.
+// One wait state lies between a scalar write of M0 and a load that takes its
+// LDS address from it.  The compiler keeps it for its own loads to LDS but not
+// for one in assembly, hence the s_nop here and below.
 __device__ __forceinline__ void dma16(v4i srd, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(voff), "s"(srd), "s"(lds_base)
                  : "memory", "m0");
@@ -66,13 +69,13 @@ __device__ __forceinline__ void dma16(v4i srd, uint32_t voff, uint32_t lds_base)
 // s_add_i32 m0, base, 0x400 for consecutive 1 KB destinations) instead of
 // computing the address into a scalar register and copying it into M0.
 __device__ __forceinline__ void dma16_m0(v4i srd, uint32_t voff, uint32_t lds_addr) {
-    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(srd), "{m0}"(lds_addr) : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(srd), "{m0}"(lds_addr) : "memory");
 }
 
 // The same with 4 bytes per lane: lane l's dword lands at lds_base + 4 * l
 // (256 bytes per instruction).  Used for the block scales.
 __device__ __forceinline__ void dma4(v4i srd, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
                  :
                  : "v"(voff), "s"(srd), "s"(lds_base)
                  : "memory", "m0");
