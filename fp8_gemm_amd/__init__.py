@@ -439,9 +439,13 @@ def grouped_gemm_contig_blockscaled(a, b, scale_a, scale_b, grp_idx, out=None, a
 # device, which need not be the current one.
 # ---------------------------------------------------------------------------
 
+PLAN_PAIR = 16
+
+
 def fused_plan(op: int, m: int, n: int, k: int) -> Plan:
     """Kernel choice of a fused or gated form (no launch).  op: 0 gemm_nt_fused, 1 gated_nt,
-    2 gemm_nt_bf16_fused, 3 gated_nt_bf16, 4 a BF16 backward product (m x n, reduced over k)."""
+    2 gemm_nt_bf16_fused, 3 gated_nt_bf16, 4 a BF16 backward product (m x n, reduced over k), 4 + PLAN_PAIR two of them
+    in one launch (the weight gradients of gated_nt_bf16_backward: N x K, reduced over M)."""
     out = Plan()
     _check(load_library().fp8_gemm_fused_plan(op, m, n, k, ctypes.byref(out)))
     return out

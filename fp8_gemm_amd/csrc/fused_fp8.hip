@@ -46,6 +46,8 @@ int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
     if (!out) return fail(FP8G_ERR_NULL, "plan output pointer is NULL");
     *out = fp8g_plan{};
     out->k_splits = 1;
+    const int products = op == 4 + FP8G_PLAN_PAIR ? 2 : 1;
+    if (products == 2) op = 4;
     if (op < 0 || op > 4) return fail(FP8G_ERR_ARG, "unknown op %d", op);
     if (op < 4) {
         if (const int st = check_sizes(m, n, k, op < 2 ? 1 : 2)) return st;
@@ -56,7 +58,7 @@ int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
     const bool gated = op == 1 || op == 3;
     ShapeClass c;
     if (op == 4) {
-        const BackwardShape b = backward_shape(m, n, k, 1);
+        const BackwardShape b = backward_shape(m, n, k, products);
         c = b.c;
         out->k_splits = b.splits;
     } else {
@@ -75,7 +77,7 @@ int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out) {
     out->variant = c == C_128x128 ? 7 : (c == C_128x256 ? 2 : 1);
     out->tile_m = c == C_256x256 ? 256 : 128;
     out->tile_n = (c == C_128x128 ? 128 : 256) / (gated ? 2 : 1);
-    out->workgroups = cdiv(m, out->tile_m) * cdiv(n, out->tile_n) * out->k_splits;
+    out->workgroups = cdiv(m, out->tile_m) * cdiv(n, out->tile_n) * out->k_splits * products;
     return ok();
 }
 

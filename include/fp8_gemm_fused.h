@@ -143,12 +143,15 @@ int64_t bf16_gated_nt_backward_workspace(int M, int N, int K);
  * Kernel choice for a problem, without launching anything (host only).
  *   op: 0 = fp8_gemm_nt_fused, 1 = fp8_gated_nt, 2 = bf16_gemm_nt_fused,
  *   3 = bf16_gated_nt, 4 = one BF16 backward product (m x n outputs, reduced
- *   over k), with k_splits splits of k.
+ *   over k), with k_splits splits of k; 4 + FP8G_PLAN_PAIR = two of them in
+ *   one launch (the weight gradients of bf16_gated_nt_backward: m = N, n = K,
+ *   k = M), with the workgroups of both.
  * Fills the plan of fp8_gemm.h: variant 1 = tiled 256 x 256, 2 = tiled 128 x
  * 256, 7 = tiled 128 x 128 (m x n of the products; the gated forms' tiles hold
  * half as many output columns), 4 = swapped decode, 0 = nothing to launch;
  * tile_m and tile_n in rows and columns of D.
  */
+#define FP8G_PLAN_PAIR 16
 int fp8_gemm_fused_plan(int op, int m, int n, int k, fp8g_plan *out);
 
 #ifdef __cplusplus
