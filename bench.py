@@ -64,7 +64,8 @@ def log(msg):
 
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
-    for f in ("kernels.hpp", "device_common.hpp", "fp8_gemm.hip"):
+    for f in ("kernels.hpp", "device_common.hpp", "fp8_gemm.hip", "fused.hpp", "fused_bf16.hpp", "fused_host.hpp",
+              "fused_fp8.hip", "fused_bf16.hip"):
         with open(os.path.join(ROOT, "fp8_gemm_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
@@ -552,11 +553,29 @@ COUNTER_TARGETS = {
                                    "N=4096 K=7168 (seed 9)"),
     "dense_4096_bf16": ("ring_kernel_dense_4096_bf16", "ring_kernel<256, 256, 4, 2, 16, 16, 0, 2, 128, 0>",
                         "dense 4096^3 BF16 GEMM, the comparison path (seed 2)"),
+    "fused_fp8_2048": ("fused_tile16_kernel_fused_2048x4096x14336", "fused_tile16_kernel<128, 256, 3, 0, 0, false, 1>",
+                       "fused FP8 product M=2048 N=4096 K=14336, residual (seed 21)"),
+    "gated_fp8_64": ("fused_decode_kernel_gated_64x14336x4096", "fused_decode_kernel<4, 4, 4, 0, 0, 2, 2>",
+                     "gated FP8 product M=64 N=14336 K=4096, silu (seed 22)"),
+    "fused_bf16_2048": ("bf16_tile_kernel_fused_2048x4096x4096", "bf16_tile_kernel<128, 256, 3, false, false, false, 1>",
+                        "fused BF16 product M=2048 N=4096 K=4096, bias, gelu_tanh, residual (seed 23)"),
+    "fused_bf16_4096": ("bf16_tile_kernel_fused_4096", "bf16_tile_kernel<256, 256, 2, false, false, false, 1>",
+                        "fused BF16 product 4096^3, bias, gelu_tanh, residual (seed 24)"),
+    "gated_bf16_grad": ("grad_kernel_gated_4096x14336x4096", "grad_kernel<true, false>",
+                        "gated BF16 backward pass M=4096 N=14336 K=4096, silu (seed 25): pre-activation gradients"),
+    "gated_bf16_token_grad": ("bf16_tile_kernel_gated_token_grad_4096x14336x4096",
+                              "bf16_tile_kernel<256, 256, 2, false, true, false, 0>",
+                              "gated BF16 backward pass M=4096 N=14336 K=4096, silu (seed 25): token gradient"),
+    "gated_bf16_weight_grad": ("bf16_tile_kernel_gated_weight_grad_4096x14336x4096",
+                               "bf16_tile_kernel<256, 256, 2, true, true, false, 0>",
+                               "gated BF16 backward pass M=4096 N=14336 K=4096, silu (seed 25): weight gradients"),
 }
 # Dense matrix-core FLOPs per SIMD per cycle of each target's instruction
 # (FP8 by default; BF16 runs at half that rate).
-MFMA_FLOPS_PER_CYCLE = {"dense_4096_bf16": 1024.0}
-MFMA_COUNT_NOTE = {"dense_4096_bf16": "each 32x32x16 BF16 instruction as 32 cycles, 1024 FLOPs per cycle"}
+FUSED_BF16_TARGETS = ("fused_bf16_2048", "fused_bf16_4096", "gated_bf16_token_grad", "gated_bf16_weight_grad")
+MFMA_FLOPS_PER_CYCLE = {"dense_4096_bf16": 1024.0, **{t: 1024.0 for t in FUSED_BF16_TARGETS}}
+MFMA_COUNT_NOTE = {"dense_4096_bf16": "each 32x32x16 BF16 instruction as 32 cycles, 1024 FLOPs per cycle",
+                   **{t: "each 16x16x32 BF16 instruction as 16 cycles, 1024 FLOPs per cycle" for t in FUSED_BF16_TARGETS}}
 COPY_PATTERN = "neg_kernel"
 PROFILE_LAUNCHES = 6
 
@@ -686,7 +705,52 @@ def profile_run(targets=None):
                                               "bytes": float(M_total * K + G * N * K + 2 * valid * N
                                                              + wc.sa.nbytes + wc.sb.nbytes)}
         del a, b, sa, sb, gi, out, wc
+    profile_fused(torch, f, on, work)
     print(json.dumps({"profile_run": True, "work": work}), flush=True)
+
+
+def profile_fused(torch, f, on, work):
+    """The fused and gated counter targets of profile_run: inputs N(0, 1), weights N(0, 0.02^2), seeded on the device."""
+    def normal(seed, *shape, std=1.0, dtype=torch.bfloat16):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        return torch.randn(*shape, generator=g, device="cuda").mul_(std).to(dtype)
+
+    def launch(name, call):
+        log(f"profile: {COUNTER_TARGETS[name][2]}")
+        for _ in range(PROFILE_LAUNCHES):
+            call()
+        torch.cuda.synchronize()
+
+    e4 = torch.float8_e4m3fn
+    if on("fused_fp8_2048"):
+        M, N, K = 2048, 4096, 14336
+        a, b, r = normal(21, M, K, dtype=e4), normal(121, N, K, dtype=e4), normal(221, M, N)
+        s = torch.full((M,), 0.01, device="cuda"), torch.full((N,), 0.02, device="cuda")
+        launch("fused_fp8_2048", lambda: f.gemm_nt_fused(a, b, *s, residual=r))
+        work["fused_fp8_2048"] = {"flops": 2.0 * M * N * K, "bytes": float(M * K + N * K + 4 * M * N + 4 * (M + N))}
+    if on("gated_fp8_64"):
+        M, N, K = 64, 14336, 4096
+        a, g, u = normal(22, M, K, dtype=e4), normal(122, N, K, dtype=e4), normal(222, N, K, dtype=e4)
+        s = torch.full((M,), 0.01, device="cuda"), torch.full((N,), 0.02, device="cuda")
+        launch("gated_fp8_64", lambda: f.gated_nt(a, g, u, s[0], s[1], s[1]))
+        work["gated_fp8_64"] = {"flops": 4.0 * M * N * K, "bytes": float(M * K + 2 * N * K + 2 * M * N + 4 * (M + 2 * N))}
+    for name, M, N, K, seed in (("fused_bf16_2048", 2048, 4096, 4096, 23), ("fused_bf16_4096", 4096, 4096, 4096, 24)):
+        if on(name):
+            a, b, r = normal(seed, M, K), normal(100 + seed, N, K, std=0.02), normal(200 + seed, M, N)
+            bias = normal(300 + seed, N, dtype=torch.float32)
+            launch(name, lambda: f.gemm_nt_bf16_fused(a, b, bias=bias, activation="gelu_tanh", residual=r))
+            work[name] = {"flops": 2.0 * M * N * K, "bytes": float(2 * (M * K + N * K + 2 * M * N) + 4 * N)}
+    if on("gated_bf16_grad") or on("gated_bf16_token_grad") or on("gated_bf16_weight_grad"):
+        M, N, K = 4096, 14336, 4096
+        a, g, u = normal(25, M, K), normal(125, N, K, std=0.02), normal(225, N, K, std=0.02)
+        grad, pre = normal(325, M, N), torch.empty(2, M, N, device="cuda")
+        f.gated_nt_bf16(a, g, u, preact=pre)
+        launch("gated_bf16_grad", lambda: f.gated_nt_bf16_backward(grad, a, g, u, pre))
+        # operations of the elementwise kernel are not counted; the gradients dP and dU are what the products read
+        work["gated_bf16_grad"] = {"flops": 0.0, "bytes": float(M * N * (2 + 8 + 4))}
+        work["gated_bf16_token_grad"] = {"flops": 4.0 * M * N * K, "bytes": float(2 * (2 * M * N + 2 * N * K + M * K))}
+        work["gated_bf16_weight_grad"] = {"flops": 4.0 * M * N * K, "bytes": float(2 * (2 * M * N + M * K + 2 * N * K))}
 
 
 def _csv_files(directory, suffix):

@@ -12,6 +12,10 @@ Functions take torch tensors on the GPU:
 * scales as float32 tensors on the device (one element, or one per expert);
 * index vectors as int32 tensors on the device;
 * outputs as ``torch.bfloat16`` tensors (allocated if not given).
+
+Autograd does not follow these calls: their outputs are plain tensors, also
+where an input requires a gradient.  The forms for training come with backward
+functions, which the caller calls (from a ``torch.autograd.Function``, say).
 """
 from __future__ import annotations
 

@@ -66,8 +66,8 @@ struct FusedParams : FusedArgs {
 // its relative precision where 1 + erf would cancel.  h(x) = erfcx(x / sqrt 2)
 // / 2 is smooth and falls like 1 / x: a polynomial of degree 7 in t = 1 / (1 +
 // 0.36 x) without constant term, fitted by least squares reweighted towards
-// the largest relative error, is within 7.9e-7 of it up to x = 13.5 (past
-// which Q underflows).  erfcf, with its two branches, made the epilogue of a
+// the largest relative error, is within 8.1e-7 of it in FP32 up to x = 13.5
+// (past which Q underflows).  erfcf, with its two branches, made the epilogue of a
 // 2048 x 4096 x 14336 product 10 us longer.
 // ---------------------------------------------------------------------------
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
@@ -387,8 +387,12 @@ __global__ __launch_bounds__(256, 1) void fused_tile16_kernel(FusedParams<EPI, t
 
 // Few tokens, FP8 and BF16.  Bound by the weights' way from memory for up to
 // 16 tokens (gated FP8 1 x 14336 x 4096 24 us, 4.9 TB/s), by the copies of
-// tokens and weights into each CU for more (64 tokens 28 us).  (Builds for one workgroup per CU, as the dense
-// form has for grids of up to 256, measured within 1% of these for two.)
+// tokens and weights into each CU for more (64 tokens 28 us): every wave
+// copies the tokens of its K steps beside 16 to 64 weight rows.  The plain
+// form's decode_rows_kernel, whose waves share one copy of the tokens, needs
+// fewer and has no fused epilogue (64 x 4096 x 14336: 22.8 us here, 18.5 the
+// plain product there).  (Builds for one workgroup per CU, as the dense form
+// has for grids of up to 256, measured within 1% of these for two.)
 template <int WAVES, int RB, int CB, int FA, int FB, int D, int EPI>
 __global__ __launch_bounds__(64 * WAVES, 2) void fused_decode_kernel(FusedParams<EPI, FA != FMT_BF16> p) {
     decode_body<WAVES, RB, CB, FA, FB, D, SCALE_CHANNEL>(p);

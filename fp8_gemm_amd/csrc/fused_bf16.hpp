@@ -344,6 +344,11 @@ __device__ __forceinline__ float act_value_exact(float z) {
 // backward products, into W [M][ldw] (gated: dU from column ldw / 2 on), whose
 // columns past N hold zeros.  Bound by memory: 6 bytes read and 2 written per
 // element (fused), 10 and 4 (gated); gated 4096 x 14336 188 us, 4.4 TB/s.
+// The rounding: the products' matrix instructions take 16-bit operands, and dZ
+// held to 16 bits as two BF16 terms would double both products' work.  Each
+// term of a gradient's sum is off by at most 2^-8 of it, independently of the
+// others, which moves the gradient about as much as its own rounding to BF16
+// does: relative errors of 0.0023 where unrounded dZ give 0.0017.
 // BIAS: also the column sums of the FP32 dZ over the block's rows into
 // part[block row][N], added over the rows in a fixed order.
 // A block is 32 groups of 8 columns x 8 rows of threads over `rows` rows: as

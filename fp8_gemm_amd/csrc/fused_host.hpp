@@ -166,7 +166,12 @@ FewShape few_shape(int64_t M, int64_t N, bool gated, int rb) {
 // to 540 measured cases (M 1 .. 2048 by nine N x K from 512 x 512 to 28672 x
 // 1024 and 1024 x 8192, FP8 and BF16, fused and gated, every class each, the
 // weights read from memory as a serving pass does): on average the choice
-// takes 0.7% longer than the fastest class.  Some, FP8 fused, few-token with
+// takes 0.7% longer than the fastest class, in 16 cases over 10%, at worst 32%
+// (FP8 fused 64 x 28672 x 1024: 64 rows 14.5 us, 128 x 128 tiles 11.0; gated
+// BF16 64 x 14336 x 4096 54.1 against 46.1).  Most of those are few-token
+// builds of 8 blocks, of which one workgroup fits a CU: the estimate is 11 to
+// 16% too low there.  Narrower outputs and more tokens than the set's are
+// extrapolated.  Some, FP8 fused, few-token with
 // 16, 32 and 64 rows | 128 x 128 | 128 x 256 tiles, in us: 64 x 14336 x 4096
 // 24.7, 20.7, 17.2 | 22.1 | 32.4; 256 x 4096 x 14336 61.1, 42.3, 33.3 | 72.0 |
 // 99.2; 512 x 4096 x 4096 36.9, 28.8, 21.7 | 23.1 | 33.2; 64 x 4096 x 4096
