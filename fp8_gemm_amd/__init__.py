@@ -47,7 +47,9 @@ SYMBOLS = ("fp8_gemm_nt", "fp8_gemm_nt_noalloc", "fp8_gemm_nt_blockscaled", "fp8
            "bf16_gemm_nt", "fp8_gemm_plan", "fp8_gemm_strerror", "fp8_gemm_abi_version",
            "fp8_gemm_nt_fused", "bf16_gemm_nt_fused", "bf16_gemm_nt_fused_backward",
            "bf16_gemm_nt_fused_backward_workspace", "fp8_gated_nt", "bf16_gated_nt", "bf16_gated_nt_backward",
-           "bf16_gated_nt_backward_workspace", "fp8_gemm_fused_plan")
+           "bf16_gated_nt_backward_workspace", "fp8_gemm_fused_plan",
+           "bf16_grouped_gemm_ragged", "bf16_grouped_gemm_ragged_backward", "int8_grouped_gemm_ragged",
+           "int8_gemm_nt_fused", "int8_quantize_rows", "fp8_gemm_experts_plan")
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
@@ -102,6 +104,18 @@ def load_library(path: str = LIB_PATH):
     lib.bf16_gated_nt_backward_workspace.restype = I64
     lib.fp8_gemm_fused_plan.argtypes = [I, I, I, I, ctypes.POINTER(Plan)]
     lib.fp8_gemm_fused_plan.restype = I
+    lib.bf16_grouped_gemm_ragged.argtypes = [P, I64, P, I64, I64, P, P, I64, I, I, I, I, P]
+    lib.bf16_grouped_gemm_ragged.restype = I
+    lib.bf16_grouped_gemm_ragged_backward.argtypes = [P, I64, P, I64, P, I64, I64, P, P, I64, P, I64, I64, I, I, I, I, P]
+    lib.bf16_grouped_gemm_ragged_backward.restype = I
+    lib.int8_grouped_gemm_ragged.argtypes = [P, I64, P, I64, I64, P, P, P, P, I64, I, I, I, I, P]
+    lib.int8_grouped_gemm_ragged.restype = I
+    lib.int8_gemm_nt_fused.argtypes = [P, I64, P, I64, P, I, P, I, P, I, P, I64, P, I64, I, I, I, P]
+    lib.int8_gemm_nt_fused.restype = I
+    lib.int8_quantize_rows.argtypes = [P, I64, P, I64, P, I, I, P]
+    lib.int8_quantize_rows.restype = I
+    lib.fp8_gemm_experts_plan.argtypes = [I, I, I, I, I, ctypes.POINTER(Plan)]
+    lib.fp8_gemm_experts_plan.restype = I
     lib.fp8_gemm_abi_version.argtypes = []
     lib.fp8_gemm_abi_version.restype = I
     _lib = lib
@@ -468,6 +482,7 @@ class _Torch:
     def __init__(self):
         import torch
         self.bf16, self.f32, self.empty = torch.bfloat16, torch.float32, torch.empty
+        self.i8, self.i32 = torch.int8, torch.int32
         self.fp8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
         self.current_device, self.guard = torch.cuda.current_device, torch.cuda.device
         # the current stream's handle without a Stream object around it, where torch offers that
@@ -775,3 +790,170 @@ def gated_nt_bf16_backward(grad_out, a, w_gate, w_up, preact, activation="silu",
           ldg, w_up.data_ptr(), ldu, pg, pu, ldp, act, _ptr(ga), ldga, _ptr(gw), _ptr(gu), ldgw, _ptr(ws),
           0 if ws is None else ws.numel(), M, N, K)
     return ga, gw, gu
+
+
+# ---------------------------------------------------------------------------
+# Experts' products over ragged groups of rows, products in 8-bit integers and
+# the quantisation of rows (include/fp8_gemm_experts.h).  As above they run on
+# the current stream of the tensors' device.
+# ---------------------------------------------------------------------------
+
+def experts_plan(op: int, m: int, n: int, k: int, groups: int = 1) -> Plan:
+    """Kernel choice of a ragged or integer form (no launch).  op: 0 grouped_gemm_ragged_bf16, 1 grouped_gemm_ragged_int8,
+    2 and 3 the token and weight gradients of grouped_gemm_ragged_bf16_backward, 4 gemm_nt_int8."""
+    out = Plan()
+    _check(load_library().fp8_gemm_experts_plan(op, m, n, k, groups, ctypes.byref(out)))
+    return out
+
+
+def _int8_only(tt, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != tt.i8:
+            raise TypeError(f"{name} must be int8, got {t.dtype}")
+
+
+def _ragged(tt, a, b, offsets):
+    """M, G, N, K of a [M, K] and b [G, N, K] with the int32 offsets [G + 1] of the experts' rows."""
+    sa, sb = a.shape, b.shape
+    if len(sa) != 2 or len(sb) != 3 or sa[1] != sb[2]:
+        raise ValueError(f"shapes {tuple(sa)} and {tuple(sb)} of a and b are not [M, K] and [G, N, K]")
+    G = sb[0]
+    if offsets.dtype != tt.i32 or tuple(offsets.shape) != (G + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor with {G + 1} elements, got {list(offsets.shape)} {offsets.dtype}")
+    return sa[0], G, sb[1], sa[1]
+
+
+def _expert_weights(b, G, N, K, grain):
+    """The row and expert strides in elements of a K-contiguous [G, N, K] operand."""
+    step, ld, unit = b.stride()
+    if unit != 1 and K > 1:
+        raise ValueError("b must be K-contiguous (stride(2) == 1)")
+    if N <= 1 or not K:
+        ld = (K + grain - 1) // grain * grain
+    return ld, step if G > 1 else N * ld
+
+
+def grouped_gemm_ragged_bf16(a, b, offsets, out=None):
+    """BF16 product of ragged groups of rows with their experts' weights:
+
+        out[r, n] = bf16(a[r] . b[g, n])    for offsets[g] <= r < offsets[g + 1]
+
+    a: bfloat16 [M, K], the rows sorted by expert; b: bfloat16 [G, N, K] with
+    any row and expert stride; offsets: int32 [G + 1] on the GPU, not
+    decreasing, from 0 to M; an expert may have any number of rows.  Rows of no
+    expert (before offsets[0], from offsets[G] on) are left as they were in
+    `out`, unset where it is allocated here.  K % 8 == 0 and N % 8 == 0.
+    """
+    tt = _tt()
+    _bf16_only(tt, a=a, b=b)
+    M, G, N, K = _ragged(tt, a, b, offsets)
+    index = _device(a, b, offsets)
+    lda = _operand(a, "a", M, K, 8)
+    ldb, step = _expert_weights(b, G, N, K, 8)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().bf16_grouped_gemm_ragged, a.data_ptr(), lda, b.data_ptr(), ldb, step,
+          offsets.data_ptr(), out.data_ptr(), ldd, M, G, N, K)
+    return out
+
+
+def grouped_gemm_ragged_bf16_backward(grad_out, a, b, offsets, a_grad=True, b_grad=True):
+    """Backward pass of grouped_gemm_ragged_bf16: (grad_a, grad_b) for the
+    gradient `grad_out` of its output (bfloat16 [M, N], unit column stride,
+    rows that start 16-byte aligned), where
+
+        grad_a[r] = bf16(grad_out[r] . b[g])                       0 for the rows of no expert
+        grad_b[g] = bf16(sum over g's rows of grad_out[r]^T . a[r])  0 for an expert without rows
+
+    What a_grad or b_grad excludes is None.
+    """
+    tt = _tt()
+    _bf16_only(tt, grad_out=grad_out, a=a, b=b)
+    M, G, N, K = _ragged(tt, a, b, offsets)
+    if tuple(grad_out.shape) != (M, N):
+        raise ValueError(f"grad_out must be a [{M}, {N}] tensor, got {list(grad_out.shape)}")
+    index = _device(a, b, offsets, grad_out)
+    lda, ldg = _operand(a, "a", M, K, 8), _operand(grad_out, "grad_out", M, N, 8)
+    ldb, step = _expert_weights(b, G, N, K, 8)
+    ga, ldga = _new(tt, M, K, a.device) if a_grad else (None, 0)
+    gb = tt.empty((G, N, K), dtype=tt.bf16, device=a.device) if b_grad else None
+    _call(tt, index, load_library().bf16_grouped_gemm_ragged_backward, grad_out.data_ptr(), ldg, a.data_ptr(), lda,
+          b.data_ptr(), ldb, step, offsets.data_ptr(), _ptr(ga), ldga, _ptr(gb), K, N * K, M, G, N, K)
+    return ga, gb
+
+
+def grouped_gemm_ragged_int8(a, b, offsets, scale_a=None, scale_b=None, out=None):
+    """The product of grouped_gemm_ragged_bf16 in 8-bit integers, with a scale for
+    each row and each expert's channel:
+
+        out[r, n] = bf16(scale_a[r] * scale_b[g, n] * a[r] . b[g, n])
+
+    a: int8 [M, K]; b: int8 [G, N, K]; scale_a: float32 [M] or None (1);
+    scale_b: float32 [G, N], contiguous, or None.  The sums are exact.
+    K % 16 == 0 and K <= 131056, N % 8 == 0.
+    """
+    tt = _tt()
+    _int8_only(tt, a=a, b=b)
+    M, G, N, K = _ragged(tt, a, b, offsets)
+    index = _device(a, b, offsets, scale_a, scale_b)
+    lda = _operand(a, "a", M, K, 16)
+    ldb, step = _expert_weights(b, G, N, K, 16)
+    sa, _ = _floats(tt, scale_a, "scale_a", M, one=False)
+    sb, _ = _floats(tt, scale_b, "scale_b", G * N, one=False)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().int8_grouped_gemm_ragged, a.data_ptr(), lda, b.data_ptr(), ldb, step, sa, sb,
+          offsets.data_ptr(), out.data_ptr(), ldd, M, G, N, K)
+    return out
+
+
+def gemm_nt_int8(a, b, scale_a=None, scale_b=None, bias=None, activation="none", residual=None, out=None):
+    """Product in 8-bit integers with bias, activation and residual in its epilogue:
+
+        out[M, N] = bf16(act(scale_a[m] * scale_b[n] * a[m] . b[n] + bias[n]) + residual[m, n])
+
+    a: int8 [M, K]; b: int8 [N, K]; everything else as for gemm_nt_fused.  The
+    sums are exact: K % 16 == 0 and K <= 131056.
+    """
+    tt = _tt()
+    _int8_only(tt, a=a, b=b)
+    M, N, K = _matrices(a, b, "b")
+    index = _device(a, b, scale_a, scale_b, bias, residual)
+    lda, ldb = _operand(a, "a", M, K, 16), _operand(b, "b", N, K, 16)
+    sa, na = _floats(tt, scale_a, "scale_a", M)
+    sb, nb = _floats(tt, scale_b, "scale_b", N)
+    bp, _ = _floats(tt, bias, "bias", N, one=False)
+    ldr = 0 if residual is None else _rows(residual, "residual", M, N, tt.bf16)
+    act = _activation(activation)
+    out, ldd = _output(tt, out, a, index, M, N)
+    _call(tt, index, load_library().int8_gemm_nt_fused, a.data_ptr(), lda, b.data_ptr(), ldb, sa, na, sb, nb, bp, act,
+          _ptr(residual), ldr, out.data_ptr(), ldd, M, N, K)
+    return out
+
+
+def quantize_rows_int8(x, codes=None, scales=None):
+    """Rows of x (bfloat16 [M, K]) in 8-bit integers: (codes, scales) with
+
+        scales[m] = max_k |x[m, k]| / 127;  codes[m, k] = round(127 x[m, k] / max_k |x[m, k]|)
+
+    rounded to the nearest whole number, halves to even.  codes: int8 [M, K],
+    scales: float32 [M], both allocated if not given.  A row of zeros has the
+    scale 0; one with an infinity or a NaN the scale NaN and codes 0.
+    K % 16 == 0.
+    """
+    tt = _tt()
+    _bf16_only(tt, x=x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be a [M, K] tensor, got {list(x.shape)}")
+    M, K = x.shape
+    index = _device(x, codes, scales)
+    ldx = _operand(x, "x", M, K, 16)
+    if codes is None:
+        ldq = (K + 15) // 16 * 16
+        codes = tt.empty((M, K), dtype=tt.i8, device=x.device)
+    else:
+        ldq = _rows(codes, "codes", M, K, tt.i8)
+    if scales is None:
+        scales = tt.empty(M, dtype=tt.f32, device=x.device)
+    elif scales.dtype != tt.f32 or tuple(scales.shape) != (M,) or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous float32 tensor with {M} elements")
+    _call(tt, index, load_library().int8_quantize_rows, x.data_ptr(), ldx, codes.data_ptr(), ldq, scales.data_ptr(), M, K)
+    return codes, scales

@@ -10,10 +10,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SRC = os.path.join(CSRC, "fp8_gemm.hip")           # the plain, block-scaled, per-channel and grouped forms
-FUSED_SRCS = [os.path.join(CSRC, f) for f in ("fused_fp8.hip", "fused_bf16.hip")]
-DEPS = [os.path.join(CSRC, f) for f in ("kernels.hpp", "device_common.hpp", "fused.hpp", "fused_bf16.hpp",
-                                        "fused_host.hpp", "host_common.hpp")] + \
-       [os.path.join(ROOT, "include", f) for f in ("fp8_gemm.h", "fp8_gemm_fused.h")]
+EXPERTS_SRCS = [os.path.join(CSRC, f) for f in ("experts_bf16.hip", "experts_int8.hip")]
+# every unit on the bodies with fused epilogues
+FUSED_SRCS = [os.path.join(CSRC, f) for f in ("fused_fp8.hip", "fused_bf16.hip")] + EXPERTS_SRCS
+DEPS = [os.path.join(CSRC, f) for f in ("kernels.hpp", "device_common.hpp", "ragged.hpp", "fused.hpp", "tile_halves.hpp",
+                                        "fused_bf16.hpp", "fused_host.hpp", "experts.hpp", "experts_host.hpp", "quantize.hpp",
+                                        "host_common.hpp")] + \
+       [os.path.join(ROOT, "include", f) for f in ("fp8_gemm.h", "fp8_gemm_fused.h", "fp8_gemm_experts.h")]
 LIB = os.path.join(HERE, "libfp8gemm.so")
 
 HIPCC_FLAGS = [

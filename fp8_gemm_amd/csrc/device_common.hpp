@@ -180,6 +180,40 @@ __device__ __forceinline__ v4f mfma16x16x64_bf16(v8i a, v8i b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a1), __builtin_bit_cast(v8bf, b1), c, 0, 0, 0);
 }
 
+// 8-bit integer operands: v_mfma_i32_16x16x64_i8, exact sums in 32 bits, one
+// instruction per 16-byte part as above (the operand layout in bytes is that of
+// the BF16 form).
+constexpr int FMT_I8 = 17;
+
+__device__ __forceinline__ v4i mfma16x16x128_i8(v8i a, v8i b, v4i c) {
+    const v4i a0 = {a[0], a[1], a[2], a[3]}, a1 = {a[4], a[5], a[6], a[7]};
+    const v4i b0 = {b[0], b[1], b[2], b[3]}, b1 = {b[4], b[5], b[6], b[7]};
+    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, b0, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, b1, c, 0, 0, 0);
+}
+
+// One 16-byte part: the sums' type and the instruction of either format.
+template <int FMT>
+struct AccOf {
+    using type = v4f;
+};
+template <>
+struct AccOf<FMT_I8> {
+    using type = v4i;
+};
+
+template <int FMT>
+__device__ __forceinline__ typename AccOf<FMT>::type mfma_half(v4u a, v4u b, typename AccOf<FMT>::type c) {
+    if constexpr (FMT == FMT_I8)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// Sums as FP32: integer sums are rounded here (to nearest even) and not before.
+__device__ __forceinline__ v4f sums_f32(v4f c) { return c; }
+__device__ __forceinline__ v4f sums_f32(v4i c) { return (v4f){(float)c[0], (float)c[1], (float)c[2], (float)c[3]}; }
+
 template <int FA, int FB>
 __device__ __forceinline__ v4f mfma16x16x128(v8i a, v8i b, v4f c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, FA, FB, 0, 0, 0, 0);

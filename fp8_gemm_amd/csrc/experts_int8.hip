@@ -1,0 +1,146 @@
+// Entry points of include/fp8_gemm_experts.h in 8-bit integers.
+#include "experts_host.hpp"
+#include "quantize.hpp"
+
+namespace {
+
+using fp8g::EPI_ACT;
+using fp8g::FMT_I8;
+using fp8g::QuantParams;
+
+constexpr int kMaxIntK = 131056;                   // 2^14 K < 2^31
+
+int check_int8_sizes(int K) {
+    if (K > kMaxIntK) return fail(FP8G_ERR_SHAPE, "K=%d exceeds %d: a sum could leave 32 bits", K, kMaxIntK);
+    return FP8G_OK;
+}
+
+template <int BM, int BN, int STAGES>
+int launch_dense(const FusedArgs &a, hipStream_t s) {
+    fp8g::Int8Params p = {};
+    static_cast<FusedArgs &>(p) = a;
+    p.tiles_m = (int)cdiv(p.M, BM);
+    p.tiles_n = (int)cdiv(p.N, BN);
+    const int64_t wgs = (int64_t)p.tiles_m * p.tiles_n;
+    if (const int st = check_grid(wgs)) return st;
+    const dim3 grid((unsigned)wgs), block(256);
+    if (p.K % 128) hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, false>), grid, block, 0, s, p);
+    return launch_status("int8 tiled kernel");
+}
+
+template <int T, int R>
+int launch_quant(const QuantParams &p, hipStream_t s) {
+    const int rows = T < 256 ? 256 / T : 1;
+    hipLaunchKernelGGL((fp8g::quantize_rows_kernel<T, R>), dim3((unsigned)cdiv(p.M, rows)), dim3(T < 256 ? 256 : T), 0, s, p);
+    return launch_status("row quantisation kernel");
+}
+
+template <int T>
+int launch_quant_chunks(const QuantParams &p, hipStream_t s) {
+    const int64_t chunks = cdiv(p.K, 8 * T);
+    if (chunks <= 1) return launch_quant<T, 1>(p, s);
+    if (chunks <= 2) return launch_quant<T, 2>(p, s);
+    if (chunks <= 4) return launch_quant<T, 4>(p, s);
+    return launch_quant<T, 8>(p, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int int8_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t ldb, int64_t b_stride,
+                             const float *scale_a, const float *scale_b, const int32_t *offsets, void *D, int64_t ldd,
+                             int M, int G, int N, int K, void *stream) {
+    int st;
+    if ((st = check_ragged_sizes(M, G, N, K, 1)) || (st = check_int8_sizes(K))) return st;
+    if (M == 0 || N == 0 || G == 0) return ok();
+    if ((st = check_operand("A", A, lda, K, 1)) || (st = check_operand("B", B, ldb, K, 1)) ||
+        (st = check_stride("B", b_stride, ldb, G, N, K, 1)) || (st = check_offsets(offsets)) ||
+        (st = check_floats("scale_a", scale_a)) || (st = check_floats("scale_b", scale_b)) ||
+        (st = check_output("D", D, ldd, N)) ||
+        (st = check_apart({area("D", D, ldd, M, N, 2)},
+                          {area("A", A, lda, M, K, 1), experts_area("B", B, ldb, b_stride, G, N, K, 1),
+                           area("scale_a", scale_a, M, 4), area("scale_b", scale_b, (int64_t)G * N, 4),
+                           area("offsets", offsets, G + 1, 4)})) ||
+        (st = check_device()))
+        return st;
+    FusedArgs p = ragged_args(A, lda, B, ldb, b_stride, D, ldd, M, G, N, K, 1);
+    p.ch_sa = scale_a; p.ch_sb = scale_b;
+    p.sa_step = p.sb_step = 1;
+    p.act = FP8G_ACT_NONE;
+    const Choice c = pick_ragged(M, G, N, K, 1, true);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (c.c == C_FEW) return launch_ragged_few_shape<FMT_I8>(p, c.few, offsets, s);
+    return launch_rows<FMT_I8, false, PLACE_GROUPS, EPI_ACT>(c.c, p, offsets, s);
+}
+
+int int8_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, const float *scale_a, int scale_a_n,
+                       const float *scale_b, int scale_b_n, const float *bias, int activation, const void *R,
+                       int64_t ldr, void *D, int64_t ldd, int M, int N, int K, void *stream) {
+    FusedArgs p = {};
+    int st;
+    if ((st = check_sizes(M, N, K, 1)) || (st = check_int8_sizes(K)) || (st = check_activation(activation))) return st;
+    if (M == 0 || N == 0) return ok();
+    if ((st = check_operand("A", A, lda, K, 1)) || (st = check_operand("B", B, ldb, K, 1)) ||
+        (st = check_output("D", D, ldd, N)) || (st = check_scale("scale_a", scale_a, scale_a_n, M, &p.sa_step)) ||
+        (st = check_scale("scale_b", scale_b, scale_b_n, N, &p.sb_step)) || (st = check_floats("bias", bias)))
+        return st;
+    if (R && (st = check_rows("R", R, ldr, N, 2, &p.r_vec))) return st;
+    if ((st = check_apart({area("D", D, ldd, M, N, 2)},
+                          {area("A", A, lda, M, K, 1), area("B", B, ldb, N, K, 1), residual_area(R, ldr, D, ldd, M, N),
+                           area("scale_a", scale_a, scale_a_n, 4), area("scale_b", scale_b, scale_b_n, 4),
+                           area("bias", bias, N, 4)})) ||
+        (st = check_device()))
+        return st;
+    p.A = static_cast<const uint8_t *>(A);
+    p.B = static_cast<const uint8_t *>(B);
+    p.B2 = p.B;
+    p.D = static_cast<uint16_t *>(D);
+    p.D2 = p.D;
+    p.lda = lda; p.ldb = ldb; p.ldb2 = ldb; p.ldd = ldd;
+    p.M = M; p.N = N; p.K = K; p.G = 1; p.cap = M;
+    p.ch_sa = scale_a; p.ch_sb = scale_b; p.bias = bias;
+    p.act = activation;
+    p.R = static_cast<const uint16_t *>(R); p.ldr = ldr;
+    p.ksplit = 1 << 30;
+    p.krows = K;
+    const Choice c = pick_class(M, N, K, 1, false);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    switch (c.c) {
+    case C_FEW: return launch_few_fmt<FMT_I8, FMT_I8, EPI_ACT>(p, c.few, s);
+    case C_128x128: return launch_dense<128, 128, 4>(p, s);
+    case C_128x256: return launch_dense<128, 256, 3>(p, s);
+    default: return launch_dense<256, 256, 2>(p, s);
+    }
+}
+
+int int8_quantize_rows(const void *X, int64_t ldx, void *Q, int64_t ldq, float *scale, int M, int K, void *stream) {
+    if (M < 0 || K < 0) return fail(FP8G_ERR_SHAPE, "negative size (M=%d K=%d)", M, K);
+    if (K % 16) return fail(FP8G_ERR_SHAPE, "K=%d is not a multiple of 16", K);
+    if (M == 0) return ok();
+    int st;
+    if (!scale) return fail(FP8G_ERR_NULL, "scale is required");
+    if ((st = check_floats("scale", scale)) || (st = check_operand("X", X, ldx, K, 2))) return st;
+    if (K > 0 && !Q) return fail(FP8G_ERR_NULL, "Q is required");
+    if (!aligned16(Q)) return fail(FP8G_ERR_ALIGN, "Q must be 16-byte aligned");
+    if (ldq < K) return fail(FP8G_ERR_STRIDE, "row stride %lld of Q below K=%d", (long long)ldq, K);
+    if (ldq % 16) return fail(FP8G_ERR_ALIGN, "row stride %lld of Q is not a multiple of 16 bytes", (long long)ldq);
+    if ((st = check_apart({area("Q", Q, ldq, M, K, 1), area("scale", scale, M, 4)}, {area("X", X, ldx, M, K, 2)})) ||
+        (st = check_grid(M)) || (st = check_device()))
+        return st;
+    QuantParams p = {};
+    p.X = static_cast<const uint16_t *>(X);
+    p.Q = static_cast<int8_t *>(Q);
+    p.scale = scale;
+    p.ldx = ldx; p.ldq = ldq;
+    p.M = M; p.K = K;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (K <= 2048 || (K <= 4096 && M >= 2048)) return launch_quant_chunks<64>(p, s);
+    if (K <= 4096 || (K <= 16384 && M >= 512)) return launch_quant_chunks<256>(p, s);
+    if (K <= 65536) return launch_quant_chunks<1024>(p, s);
+    hipLaunchKernelGGL(fp8g::quantize_long_rows_kernel, dim3((unsigned)M), dim3(1024), 0, s, p);
+    return launch_status("row quantisation kernel");
+}
+
+}  // extern "C"

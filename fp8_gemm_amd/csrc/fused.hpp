@@ -25,6 +25,7 @@ constexpr int EPI_PARTIAL = 3;
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
 struct FusedArgs : GemmParams {
+    static constexpr bool kIntSums = false;        // the tiles' sums are 32-bit integers
     // Gated: the second weight matrix and its channel scales (p.B / ch_sb: the
     // first).  K-strided B of the backward pass: the rows of K steps from
     // ksplit on.
@@ -52,6 +53,25 @@ template <int E, bool SCALED>
 struct FusedParams : FusedArgs {
     static constexpr int kEpilogue = E;
     static constexpr bool kScaled = SCALED;
+};
+
+// 8-bit integers (experts.hpp): the sums are staged as they are and become FP32
+// (rounded to nearest even) where the epilogue reads them.  Converted before,
+// they took registers that the 256 x 256 tile does not have (5 spilled).
+struct Int8Params : FusedParams<EPI_ACT, true> {
+    static constexpr bool kIntSums = true;
+};
+
+// Over ragged groups of rows (ragged.hpp): expert g's weights begin b_gstride
+// bytes after those of expert g - 1, its channel scales N floats, its weight
+// gradient d_gstride elements.  rows: PLACE_SUMS, the number of token rows (M
+// and N are the gradient's).  Scales come with 8-bit integers only.
+template <int E, bool SCALED, int PLACE>
+struct RaggedParams : FusedParams<E, SCALED> {
+    static constexpr int kPlace = PLACE;
+    static constexpr bool kIntSums = SCALED;
+    const int32_t *offsets;
+    int rows;
 };
 
 // ---------------------------------------------------------------------------
@@ -299,7 +319,15 @@ __device__ __forceinline__ void fused_store_rows(const P &p, const uint8_t *smem
         const v4f lo = *reinterpret_cast<const v4f *>(row + (c ^ ((uint32_t)s & 15u)) * 16);
         const v4f hi = *reinterpret_cast<const v4f *>(row + ((c + 1) ^ ((uint32_t)s & 15u)) * 16);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) { z[e] = lo[e]; z[4 + e] = hi[e]; }
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (P::kIntSums) {           // (the vectors as wholes: a bit cast of one element takes the first)
+                z[e] = (float)__builtin_bit_cast(v4i, lo)[e];
+                z[4 + e] = (float)__builtin_bit_cast(v4i, hi)[e];
+            } else {
+                z[e] = lo[e];
+                z[4 + e] = hi[e];
+            }
+        }
     };
     auto write8 = [&](int m, const float (&o)[8]) {
         const v2u lo = pack_bf16x4(o[0], o[1], o[2], o[3]), hi = pack_bf16x4(o[4], o[5], o[6], o[7]);

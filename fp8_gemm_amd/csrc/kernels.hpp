@@ -37,6 +37,7 @@
 #pragma once
 
 #include "device_common.hpp"
+#include "ragged.hpp"
 
 namespace fp8g {
 
@@ -52,6 +53,7 @@ enum { EPI_STORE = 0, EPI_ACT = 1, EPI_GATED = 2 };
 
 struct GemmParams {
     static constexpr int kEpilogue = EPI_STORE;
+    static constexpr int kPlace = PLACE_DENSE;
     const uint8_t *A;          // tokens: [m x K] rows of lda bytes (per group: + g * a_gstride)
     const uint8_t *B;          // weights: [n x K] rows of ldb bytes (per group: + g * b_gstride)
     uint16_t *D;               // BF16 [m x N], ldd elements (per group: + g * d_gstride)
@@ -1618,6 +1620,9 @@ template <int WAVES, int RB, int CB, int FA, int FB, int D, int SCL, class P>
 __device__ __forceinline__ void decode_body(P p) {
     constexpr int EPI = P::kEpilogue;
     constexpr bool GATED = EPI == EPI_GATED;
+    constexpr bool RAGGED = P::kPlace == PLACE_GROUPS;
+    static_assert(!RAGGED || EPI == EPI_ACT, "ragged groups: fused epilogue");
+    using Acc = typename AccOf<FA>::type;
     constexpr bool BLK = SCL == SCALE_BLOCK, CHN = SCL == SCALE_CHANNEL;
     constexpr int OUT = GATED ? 8 * RB : 16 * RB;  // output columns per workgroup
     static_assert(!GATED || RB % 2 == 0, "gated: blocks of both matrices");
@@ -1645,6 +1650,17 @@ __device__ __forceinline__ void decode_body(P p) {
     // remaining kernel arguments only after the branch, a second round of
     // scalar loads that cost every launch ~0.3 us.  Unsplit, grid y counts
     // the 64-token tiles of the small-shape class.
+    int tm0 = 0, rows_t = 0;
+    if constexpr (RAGGED) {
+        // 16 CB rows of one expert, times its weights
+        RaggedTiles<16 * CB, false> tiles{p.offsets, p.G, p.M, lane, 0, 0, 0};
+        typename RaggedTiles<16 * CB, false>::Spot spot;
+        if (!tiles.find((int)blockIdx.y, spot, true)) return;
+        tm0 = spot.m0;
+        rows_t = spot.rows;
+        p.B += (int64_t)spot.g * p.b_gstride;
+        if (P::kScaled && p.ch_sb) p.ch_sb += (int64_t)spot.g * p.N;
+    }
     const int splits = EPI == EPI_STORE ? max(p.splits, 1) : 1;
     const int nb = blockIdx.x;
     const int sp = splits > 1 ? (int)blockIdx.y : 0;
@@ -1662,8 +1678,10 @@ __device__ __forceinline__ void decode_body(P p) {
     }
     // token tile: all M tokens (M <= 64), or 64-row tile blockIdx.y of them
     // (the small-shape class, never split over K)
-    const int tm0 = splits > 1 ? 0 : (int)blockIdx.y * 64;
-    const int rows_t = live ? min(p.M - tm0, 64) : 0;
+    if constexpr (!RAGGED) {
+        tm0 = splits > 1 ? 0 : (int)blockIdx.y * 64;
+        rows_t = live ? min(p.M - tm0, 64) : 0;
+    }
     const v4i srdT = make_srd(p.A + (int64_t)tm0 * p.lda, rows_bytes(rows_t, p.lda));
     const int nk = (p.K + 127) / 128;
     // this split's K steps [kt0, kt1), taken by the waves round-robin
@@ -1744,11 +1762,11 @@ __device__ __forceinline__ void decode_body(P p) {
     const uint32_t ro1 = (uint32_t)r16 * 128u + (((uint32_t)(4 + kg) ^ rkey) * 16u);
     const uint8_t *wbase = smem + wave * WRING;
 
-    v4f acc[RB][CB];
+    Acc acc[RB][CB];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
-        for (int c = 0; c < CB; ++c) acc[r][c] = (v4f){0, 0, 0, 0};
+        for (int c = 0; c < CB; ++c) acc[r][c] = (Acc){0, 0, 0, 0};
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) issue(d, d);
     for (int s0 = 0; s0 < my; s0 += D) {
@@ -1774,8 +1792,9 @@ __device__ __forceinline__ void decode_body(P p) {
                 const int ssa = BLK ? slot[NB * 2048 + c * 16 + r16] : 127;
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
-                    if (BLK) acc[r][c] = mfma16x16x128_s<FB, FA>(wf[r], tf, acc[r][c], ssb, ssa);
+                    if constexpr (BLK) acc[r][c] = mfma16x16x128_s<FB, FA>(wf[r], tf, acc[r][c], ssb, ssa);
                     else if constexpr (FA == FMT_BF16) acc[r][c] = mfma16x16x64_bf16(wf[r], tf, acc[r][c]);
+                    else if constexpr (FA == FMT_I8) acc[r][c] = mfma16x16x128_i8(wf[r], tf, acc[r][c]);
                     else acc[r][c] = mfma16x16x128<FB, FA>(wf[r], tf, acc[r][c]);
                 }
             }
@@ -1788,7 +1807,7 @@ __device__ __forceinline__ void decode_body(P p) {
     // Sum the WAVES partial accumulators (fixed order), then scale, round and
     // store: register q of a 16x16 block holds weight row 4 kg + q and token
     // column r16, so a lane writes four consecutive outputs of one token row.
-    v4f *red = reinterpret_cast<v4f *>(smem);
+    Acc *red = reinterpret_cast<Acc *>(smem);
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
@@ -1802,10 +1821,10 @@ __device__ __forceinline__ void decode_body(P p) {
         // c; wave w takes blocks w, w + WAVES, ... (gated: both matrices' sums)
         constexpr int QB = OUT / 16;
         auto total = [&](int idx) {
-            v4f sum = red[idx * 64 + lane];
+            Acc sum = red[idx * 64 + lane];
 #pragma unroll
             for (int w = 1; w < WAVES; ++w) sum += red[(w * NBLK + idx) * 64 + lane];
-            return sum;
+            return sums_f32(sum);
         };
         for (int o = wave; o < QB * CB; o += WAVES) {
             const int q = o / CB, c = o % CB;
@@ -1821,9 +1840,9 @@ __device__ __forceinline__ void decode_body(P p) {
     for (int j = 0; j < PER; ++j) {
         const int idx = wave + WAVES * j;
         if (idx >= NBLK) break;
-        v4f sum = red[idx * 64 + lane];
+        v4f sum = sums_f32(red[idx * 64 + lane]);
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) sum += red[(w * NBLK + idx) * 64 + lane];
+        for (int w = 1; w < WAVES; ++w) sum += sums_f32(red[(w * NBLK + idx) * 64 + lane]);
         sums[j] = sum;
     }
     if (splits > 1) {
