@@ -28,8 +28,8 @@ __global__ __launch_bounds__(256, 2) void ragged_decode_kernel(RaggedParams<EPI_
 }
 
 // The dense product in 8-bit integers (few tokens: fused_decode_kernel).
-template <int BM, int BN, int STAGES, bool TAIL>
-__global__ __launch_bounds__(256, 1) void int8_tile_kernel(Int8Params p) {
+template <int BM, int BN, int STAGES, bool TAIL, int EPI>
+__global__ __launch_bounds__(256, 1) void int8_tile_kernel(Int8Params<EPI> p) {
     tile_halves_body<BM, BN, STAGES, FMT_I8, false, false, TAIL, PLACE_DENSE>(p);
 }
 

@@ -13,7 +13,7 @@ int launch_sums_shape(const FusedArgs &a, const int32_t *offsets, int rows, hipS
     p.tiles_n = (int)cdiv(p.N, BN);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     if (const int st = check_grid(tiles * p.G)) return st;
-    const dim3 grid((unsigned)tiles, (unsigned)p.G), block(256);
+    const dim3 grid((unsigned)persistent_grid(tiles * p.G)), block(256);
     hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, FMT_BF16, true, true, false, PLACE_SUMS, EPI_STORE>), grid,
                        block, 0, s, p);
     return launch_status("ragged weight gradient kernel");
@@ -39,8 +39,9 @@ int fp8_gemm_experts_plan(int op, int m, int n, int k, int groups, fp8g_plan *ou
         tiles = cdiv(n, kClassRows[c - C_128x128]) * groups;
         cols = k;
     } else {
-        const Choice choice = op == 4 ? pick_class(m, n, k, 1, false)
-                                      : op == 2 ? pick_ragged(m, groups, k, n, 2, false) : pick_ragged(m, groups, n, k, unit, true);
+        const Choice choice = op == 4 ? pick_dense(m, n, k, n % 8 == 0)
+                                      : op == 2 ? pick_ragged(R_TOKEN_GRAD, m, groups, k, n)
+                                                : pick_ragged(op == 0 ? R_BF16 : R_INT8, m, groups, n, k);
         c = choice.c;
         if (c == C_FEW) {
             out->variant = 4;
@@ -68,14 +69,14 @@ int bf16_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t 
     if (M == 0 || N == 0 || G == 0) return ok();
     if ((st = check_operand("A", A, lda, K, 2)) || (st = check_operand("B", B, ldb, K, 2)) ||
         (st = check_stride("B", b_stride, ldb, G, N, K, 2)) || (st = check_offsets(offsets)) ||
-        (st = check_output("D", D, ldd, N)) ||
+        (st = check_tile_output("D", D, ldd, N)) ||
         (st = check_apart({area("D", D, ldd, M, N, 2)},
                           {area("A", A, lda, M, K, 2), experts_area("B", B, ldb, b_stride, G, N, K, 2),
                            area("offsets", offsets, G + 1, 4)})) ||
         (st = check_device()))
         return st;
     FusedArgs p = ragged_args(A, lda, B, ldb, b_stride, D, ldd, M, G, N, K, 2);
-    const Choice c = pick_ragged(M, G, N, K, 2, true);
+    const Choice c = pick_ragged(R_BF16, M, G, N, K);
     if (c.c != C_FEW) return launch_rows<FMT_BF16, false, PLACE_GROUPS, EPI_STORE>(c.c, p, offsets, static_cast<hipStream_t>(stream));
     p.K *= 2;
     return launch_ragged_few_shape<FMT_BF16>(p, c.few, offsets, static_cast<hipStream_t>(stream));
@@ -94,9 +95,9 @@ int bf16_grouped_gemm_ragged_backward(const void *dD, int64_t ldg, const void *A
     const bool sums = M > 0 && N > 0 && G > 0;       // anything to add up
     if ((st = check_offsets(offsets)) || (sums && (st = check_operand("dD", dD, ldg, N, 2)))) return st;
     if (want_a && ((sums && ((st = check_operand("B", B, ldb, K, 2)) || (st = check_stride("B", b_stride, ldb, G, N, K, 2)))) ||
-                   (st = check_output("dA", dA, ldda, K))))
+                   (st = check_tile_output("dA", dA, ldda, K))))
         return st;
-    if (want_b && ((sums && (st = check_operand("A", A, lda, K, 2))) || (st = check_output("dB", dB, lddb, K)) ||
+    if (want_b && ((sums && (st = check_operand("A", A, lda, K, 2))) || (st = check_tile_output("dB", dB, lddb, K)) ||
                    (st = check_stride("dB", db_stride, lddb, G, N, K, 2))))
         return st;
     if ((st = check_apart({area("dA", want_a ? dA : nullptr, ldda, M, K, 2),
@@ -109,7 +110,7 @@ int bf16_grouped_gemm_ragged_backward(const void *dD, int64_t ldg, const void *A
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (want_a) {
         const FusedArgs p = ragged_args(dD, ldg, B, ldb, b_stride, dA, ldda, M, G, K, N, 2);
-        if ((st = launch_rows<FMT_BF16, true, PLACE_REST, EPI_STORE>(pick_ragged(M, G, K, N, 2, false).c, p, offsets, s))) return st;
+        if ((st = launch_rows<FMT_BF16, true, PLACE_REST, EPI_STORE>(pick_ragged(R_TOKEN_GRAD, M, G, K, N).c, p, offsets, s))) return st;
     }
     if (want_b) {
         FusedArgs p = ragged_args(dD, ldg, A, lda, 0, dB, lddb, N, G, K, M, 2);

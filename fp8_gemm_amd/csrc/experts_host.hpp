@@ -22,6 +22,13 @@ int check_ragged_sizes(int M, int G, int N, int K, int unit) {
     return FP8G_OK;
 }
 
+// A BF16 output whose tiles are addressed with 32-bit offsets.
+int check_tile_output(const char *name, const void *ptr, int64_t ld, int cols) {
+    if (const int st = check_output(name, ptr, ld, cols)) return st;
+    if (2 * ld > kMaxRowStride) return fail(FP8G_ERR_STRIDE, "row stride of %s above %lld bytes", name, (long long)kMaxRowStride);
+    return FP8G_OK;
+}
+
 int check_offsets(const int32_t *offsets) {
     if (!offsets) return fail(FP8G_ERR_NULL, "offsets is required");
     if (!aligned4(offsets)) return fail(FP8G_ERR_ALIGN, "offsets must be 4-byte aligned");
@@ -51,39 +58,75 @@ int64_t tiles_bound(int64_t M, int64_t segments, int rows) {
 }
 
 // ---------------------------------------------------------------------------
-// Shape classes of the ragged products: the one with the smallest estimated
-// time, by fused_host.hpp's estimates with the number of tiles that M rows
+// Shape classes of the ragged and integer products: the one with the smallest
+// estimated time, as in fused_host.hpp, with the number of tiles that M rows
 // divided among G experts make on average (half a tile more per expert than
 // whole tiles alone).
+//
+// The constants (us; the persistent kernels: launch, and per round of 256
+// workgroups a fixed part and the K steps) are fitted to 3047 measured cases,
+// every class each: 2 .. 160 experts, 1 .. 65536 rows divided unevenly, N 32 ..
+// 14336, K 64 .. 8192, the weights read from memory.  On average the choice
+// takes longer than the fastest class by 3.1% (BF16), 1.9% (8-bit integers),
+// 0.7% (token gradients) and 0.8% (weight gradients); with the dense products'
+// constants it was 6.1, 6.3, 1.0 and 5.8%.  Most of what is left are products of
+// few columns below 15 us, where the number of rows of the largest expert
+// matters, which the host does not know: at worst 2.1 times (BF16 2060 rows
+// of 41 experts, 56 x 288: 13.7 against 6.5 us) and 1.65 times (integers,
+// 12264 rows of 101 experts, 160 x 6000: 74 against 45 us).
 // ---------------------------------------------------------------------------
+enum RaggedOp { R_BF16, R_INT8, R_TOKEN_GRAD, R_WEIGHT_GRAD };
+
+constexpr ClassCost kRaggedCost[4][3] = {{{1.7, 2.6, 0.343, 0.244}, {1.1, 4.0, 0.613, 0.408}, {1.2, 5.5, 0.949, 0.422}},
+                                         {{3.2, 3.6, 0.332, 0.217}, {3.2, 5.5, 0.584, 0.345}, {2.1, 8.4, 0.977, 0.395}},
+                                         {{2.4, 2.7, 0.380, 0.201}, {2.1, 4.1, 0.808, 0.185}, {2.4, 5.1, 1.006, 0.336}},
+                                         {{3.4, 2.3, 0.488, 0.148}, {4.0, 3.1, 1.082, 0.132}, {3.1, 4.5, 1.385, 0.360}}};
+struct FewCost {
+    double launch, round, copy, memory;            // copy: bytes per ns and CU; memory: bytes per us / 1e6
+};
+constexpr FewCost kRaggedFew[2] = {{3.6, 2.3, 75.7, 5.8}, {4.4, 2.4, 77.2, 6.2}};
+
 double expected_tiles(double M, double live, int rows) {
     const double t = M / rows + 0.5 * live;
     return t > live ? t : live;
 }
 
-Choice pick_ragged(int64_t M, int64_t G, int64_t N, int64_t K, int unit, bool few) {
+double ragged_time(RaggedOp op, int c, double tiles, double steps) {
+    const ClassCost &k = kRaggedCost[op][c];
+    const double full = tiles < 256 ? tiles / 256.0 : 1.0;
+    return k.launch + (double)cdiv((int64_t)tiles, 256) * (k.wave + steps * (k.step + k.load * full));
+}
+
+// M rows [K] of G experts times weights [N][K] (op R_TOKEN_GRAD: N and K are
+// those of the gradient's product).
+Choice pick_ragged(RaggedOp op, int64_t M, int64_t G, int64_t N, int64_t K) {
+    const int unit = op == R_INT8 ? 1 : 2;
     const double kbytes = (double)K * unit, live = (double)(G < 1 ? 1 : (G < M ? G : M));
-    const double memory = 2.0 + (kbytes * ((double)N * live + (double)M) + 2.0 * (double)M * (double)N) / 5.0e6;
-    auto floored = [&](double t) { return (t > memory ? t : memory) + 0.05 * t; };
+    const double bytes = kbytes * ((double)N * live + (double)M) + 2.0 * (double)M * (double)N;
     Choice best = {C_256x256, {}};
     double least = 1e300;
-    for (int cb = 1; few && cb <= 4; cb *= 2) {
+    auto consider = [&](double t, double memory, const Choice &c) {
+        t = (t > 2.0 + memory ? t : 2.0 + memory) + 0.05 * t;
+        if (t < least) least = t, best = c;
+    };
+    for (int cb = 1; op <= R_INT8 && cb <= 4; cb *= 2) {
         const int64_t tiles = tiles_bound(M, G, 16 * cb);
         if (tiles > 65535) continue;               // (grid y)
+        const FewCost &k = kRaggedFew[op];
         for (int rb = 1; rb <= 4; rb *= 2) {
             int fit = 160 * 1024 / (kFewWaves * (rb + cb) * 2048 * few_slots(rb, cb));
             if (fit > 3) fit = 3;
-            double rounds = (double)cdiv(N, 16 * rb) * expected_tiles((double)M, live, 16 * cb) / 256.0;
+            const double wgs = (double)cdiv(N, 16 * rb) * expected_tiles((double)M, live, 16 * cb);
+            double rounds = fit == 1 ? (double)cdiv((int64_t)wgs, 256) : wgs / 256.0;
             if (rounds < 1.0) rounds = 1.0;
-            const double t = floored(2.5 + rounds * (1.5 / fit + 16.0 * (rb + cb) * kbytes / 70e3));
-            if (t < least) least = t, best = Choice{C_FEW, FewShape{rb, cb, cdiv(N, 16 * rb) * tiles}};
+            consider(k.launch + rounds * (k.round / fit + 16.0 * (rb + cb) * kbytes / (k.copy * 1e3)), bytes / (k.memory * 1e6),
+                     Choice{C_FEW, FewShape{rb, cb, cdiv(N, 16 * rb) * tiles}});
         }
     }
-    for (int c = 0; c < 3; ++c) {
-        const double tiles = expected_tiles((double)M, live, (int)kClassRows[c]) * (double)cdiv(N, kClassCols[c]);
-        const double t = floored(tiled_time(c, 2, (int64_t)tiles, cdiv(K * unit, 128)));
-        if (t < least) least = t, best = Choice{(ShapeClass)(C_128x128 + c), {}};
-    }
+    for (int c = 0; c < 3; ++c)
+        consider(ragged_time(op, c, expected_tiles((double)M, live, (int)kClassRows[c]) * (double)cdiv(N, kClassCols[c]),
+                             (double)cdiv(K * unit, 128)),
+                 bytes / 5.0e6, Choice{(ShapeClass)(C_128x128 + c), {}});
     return best;
 }
 
@@ -91,10 +134,23 @@ Choice pick_ragged(int64_t M, int64_t G, int64_t N, int64_t K, int unit, bool fe
 ShapeClass pick_sums(int64_t M, int64_t G, int64_t N, int64_t K) {
     ShapeClass best = C_256x256;
     double least = 1e300;
+    const double steps = (double)M / (64.0 * (double)(G > 0 ? G : 1)) + 0.5;
     for (int c = 0; c < 3; ++c) {
-        const int64_t tiles = cdiv(N, kClassRows[c]) * cdiv(K, kClassCols[c]) * G;
-        const double t = tiled_time(c, 2, tiles, cdiv(M, 64 * (G > 0 ? G : 1)));
+        const double t = ragged_time(R_WEIGHT_GRAD, c, (double)(cdiv(N, kClassRows[c]) * cdiv(K, kClassCols[c]) * G), steps);
         if (t < least) least = t, best = (ShapeClass)(C_128x128 + c);
+    }
+    return best;
+}
+
+// The dense integer product: few tokens or not as for FP8; `direct`: the
+// tiled kernel is the persistent one.
+Choice pick_dense(int64_t M, int64_t N, int64_t K, bool direct) {
+    Choice best = pick_class(M, N, K, 1, false);
+    if (best.c == C_FEW || !direct) return best;
+    double least = 1e300;
+    for (int c = 0; c < 3; ++c) {
+        const double t = ragged_time(R_INT8, c, (double)(cdiv(M, kClassRows[c]) * cdiv(N, kClassCols[c])), (double)cdiv(K, 128));
+        if (t < least) least = t, best.c = (ShapeClass)(C_128x128 + c);
     }
     return best;
 }
@@ -114,13 +170,16 @@ int check_grid(int64_t workgroups) {
     return FP8G_OK;
 }
 
+// Persistent workgroups: one per CU.
+int64_t persistent_grid(int64_t tiles) { return tiles < 256 ? tiles : 256; }
+
 template <int BM, int BN, int STAGES, int FMT, bool TB, int PLACE, int EPI>
 int launch_rows_shape(const FusedArgs &a, const int32_t *offsets, hipStream_t s) {
     auto p = with_offsets<EPI, FMT == fp8g::FMT_I8, PLACE>(a, offsets);
     p.tiles_n = (int)cdiv(p.N, BN);
     const int64_t wgs = tiles_bound(p.M, p.G + (PLACE == PLACE_REST ? 2 : 0), BM) * p.tiles_n;
     if (const int st = check_grid(wgs)) return st;
-    const dim3 grid((unsigned)wgs), block(256);
+    const dim3 grid((unsigned)persistent_grid(wgs)), block(256);
     if (p.K % (FMT == fp8g::FMT_I8 ? 128 : 64))
         hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, FMT, false, TB, true, PLACE, EPI>), grid, block, 0, s, p);
     else

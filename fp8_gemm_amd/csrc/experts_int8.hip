@@ -5,6 +5,7 @@
 namespace {
 
 using fp8g::EPI_ACT;
+using fp8g::EPI_SCALED;
 using fp8g::FMT_I8;
 using fp8g::QuantParams;
 
@@ -15,18 +16,29 @@ int check_int8_sizes(int K) {
     return FP8G_OK;
 }
 
-template <int BM, int BN, int STAGES>
-int launch_dense(const FusedArgs &a, hipStream_t s) {
-    fp8g::Int8Params p = {};
+template <int BM, int BN, int STAGES, int EPI>
+int launch_epilogue(const FusedArgs &a, hipStream_t s) {
+    fp8g::Int8Params<EPI> p = {};
     static_cast<FusedArgs &>(p) = a;
     p.tiles_m = (int)cdiv(p.M, BM);
     p.tiles_n = (int)cdiv(p.N, BN);
     const int64_t wgs = (int64_t)p.tiles_m * p.tiles_n;
     if (const int st = check_grid(wgs)) return st;
-    const dim3 grid((unsigned)wgs), block(256);
-    if (p.K % 128) hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, false>), grid, block, 0, s, p);
+    const dim3 grid((unsigned)(EPI == EPI_SCALED ? persistent_grid(wgs) : wgs)), block(256);
+    if (p.K % 128) hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, true, EPI>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, false, EPI>), grid, block, 0, s, p);
     return launch_status("int8 tiled kernel");
+}
+
+// Scales and bias alone, in whole chunks of 8 columns, take the persistent
+// form, whose offsets into a tile's output are 32-bit.
+bool direct_epilogue(const FusedArgs &a) {
+    return a.act == FP8G_ACT_NONE && !a.R && a.N % 8 == 0 && 2 * a.ldd <= kMaxRowStride;
+}
+
+template <int BM, int BN, int STAGES>
+int launch_dense(const FusedArgs &a, bool direct, hipStream_t s) {
+    return direct ? launch_epilogue<BM, BN, STAGES, EPI_SCALED>(a, s) : launch_epilogue<BM, BN, STAGES, EPI_ACT>(a, s);
 }
 
 template <int T, int R>
@@ -58,7 +70,7 @@ int int8_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t 
     if ((st = check_operand("A", A, lda, K, 1)) || (st = check_operand("B", B, ldb, K, 1)) ||
         (st = check_stride("B", b_stride, ldb, G, N, K, 1)) || (st = check_offsets(offsets)) ||
         (st = check_floats("scale_a", scale_a)) || (st = check_floats("scale_b", scale_b)) ||
-        (st = check_output("D", D, ldd, N)) ||
+        (st = check_tile_output("D", D, ldd, N)) ||
         (st = check_apart({area("D", D, ldd, M, N, 2)},
                           {area("A", A, lda, M, K, 1), experts_area("B", B, ldb, b_stride, G, N, K, 1),
                            area("scale_a", scale_a, M, 4), area("scale_b", scale_b, (int64_t)G * N, 4),
@@ -69,10 +81,10 @@ int int8_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t 
     p.ch_sa = scale_a; p.ch_sb = scale_b;
     p.sa_step = p.sb_step = 1;
     p.act = FP8G_ACT_NONE;
-    const Choice c = pick_ragged(M, G, N, K, 1, true);
+    const Choice c = pick_ragged(R_INT8, M, G, N, K);
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (c.c == C_FEW) return launch_ragged_few_shape<FMT_I8>(p, c.few, offsets, s);
-    return launch_rows<FMT_I8, false, PLACE_GROUPS, EPI_ACT>(c.c, p, offsets, s);
+    return launch_rows<FMT_I8, false, PLACE_GROUPS, EPI_SCALED>(c.c, p, offsets, s);
 }
 
 int int8_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, const float *scale_a, int scale_a_n,
@@ -105,13 +117,14 @@ int int8_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, c
     p.R = static_cast<const uint16_t *>(R); p.ldr = ldr;
     p.ksplit = 1 << 30;
     p.krows = K;
-    const Choice c = pick_class(M, N, K, 1, false);
+    const bool direct = direct_epilogue(p);
+    const Choice c = pick_dense(M, N, K, direct);
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (c.c) {
     case C_FEW: return launch_few_fmt<FMT_I8, FMT_I8, EPI_ACT>(p, c.few, s);
-    case C_128x128: return launch_dense<128, 128, 4>(p, s);
-    case C_128x256: return launch_dense<128, 256, 3>(p, s);
-    default: return launch_dense<256, 256, 2>(p, s);
+    case C_128x128: return launch_dense<128, 128, 4>(p, direct, s);
+    case C_128x256: return launch_dense<128, 256, 3>(p, direct, s);
+    default: return launch_dense<256, 256, 2>(p, direct, s);
     }
 }
 

@@ -21,6 +21,8 @@ namespace fp8g {
 
 // One split of a backward product: FP32 sums into the workspace.
 constexpr int EPI_PARTIAL = 3;
+// Scales and bias alone, applied in the accumulators' layout (tile_halves.hpp).
+constexpr int EPI_SCALED = 4;
 
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
@@ -58,7 +60,8 @@ struct FusedParams : FusedArgs {
 // 8-bit integers (experts.hpp): the sums are staged as they are and become FP32
 // (rounded to nearest even) where the epilogue reads them.  Converted before,
 // they took registers that the 256 x 256 tile does not have (5 spilled).
-struct Int8Params : FusedParams<EPI_ACT, true> {
+template <int E>
+struct Int8Params : FusedParams<E, true> {
     static constexpr bool kIntSums = true;
 };
 
@@ -281,7 +284,7 @@ __device__ __forceinline__ void copy_tile_terms(const P &p, uint8_t *terms, uint
         if (GATED && wave >= 2) copy(p.ch_sb2, p.sb_step, n0, rows_n, idx - 128, 256, 1.0f);
         else copy(p.ch_sb, p.sb_step, n0, rows_n, idx, 256, 1.0f);
     }
-    if (P::kEpilogue == EPI_ACT) copy(p.bias, 1, n0, rows_n, idx, 512, 0.0f);
+    if (P::kEpilogue == EPI_ACT || P::kEpilogue == EPI_SCALED) copy(p.bias, 1, n0, rows_n, idx, 512, 0.0f);
 }
 
 template <int BN, int ROWS, class P, class RowOf, class Stage>

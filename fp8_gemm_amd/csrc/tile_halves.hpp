@@ -53,6 +53,12 @@ namespace fp8g {
 // end behind the last of them, and only where they begin comes from the
 // offsets (one round of loads and a scan over the experts before the first
 // copy).
+//
+// Persistent workgroups (every placement but the dense BF16 products'): one per
+// CU, each on tiles blockIdx.x, + gridDim.x, ..., so that the number of tiles
+// need not be known to the host.  A tile's first copies go out before the
+// tile before it is written, which hides their way from memory, the launch and
+// the offsets behind the epilogue.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int strided_key(int k) { return 2 * (k & 3) + ((k >> 3) & 1); }
 
@@ -92,52 +98,60 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     static_assert(CPA % 4 == 0 && CPB % 4 == 0, "copies split evenly");
     static_assert(STAGES >= 2 && CPW * (STAGES - 1) < 64, "ring");
     static_assert(FPASS <= 2 && RW % 16 == 0, "epilogue rows");
-    constexpr int TERMS = EPI == EPI_ACT ? 3 * 1024 : 0;   // (copy_tile_terms; the biases are used)
-    static_assert(RING + TERMS <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING + TERMS];
+    // Persistent workgroups with the direct epilogue (see above).
+    constexpr bool PERSIST = PLACE != PLACE_DENSE || EPI == EPI_SCALED;
+    static_assert(!PERSIST || EPI == EPI_STORE || EPI == EPI_SCALED, "direct epilogues");
+    // row scales, column scales and biases (copy_tile_terms); persistent: of
+    // two tiles in turn
+    constexpr int TERMS = EPI == EPI_ACT || EPI == EPI_SCALED ? 3 * 1024 : 0;
+    constexpr int STAGE_AT = RING + 2 * TERMS, STAGE = 2048;       // direct epilogue: 16 rows x 64 columns per wave
+    constexpr int SMEM = PERSIST ? STAGE_AT + WAVES * STAGE : RING + TERMS;
+    static_assert(SMEM <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
-
     constexpr int BNO = GATED ? BN / 2 : BN;       // output columns of a tile
-    int tm, tn, m0, rows_m;
+
+    // ---- the tiles of this workgroup
+    struct Where {
+        int g, m0, rows, tn;                       // expert, first row and rows, column of tiles
+    };
+    RaggedTiles<BM, PLACE == PLACE_REST> tiles = {};
+    int row_tiles = 0;
     if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
-        RaggedTiles<BM, PLACE == PLACE_REST> tiles{p.offsets, p.G, p.M, lane, 0, 0, 0};
-        const int count = tiles.count();
-        if ((int)blockIdx.x >= count * p.tiles_n) return;
-        tile_coords<true>(blockIdx.x, count, p.tiles_n, tm, tn);
-        typename RaggedTiles<BM, PLACE == PLACE_REST>::Spot spot;
-        if (!tiles.find(tm, spot, false)) return;
-        m0 = spot.m0;
-        rows_m = spot.rows;
-        if (spot.g < 0) p.K = 0;                   // (the empty sum)
-        else p.B += (int64_t)spot.g * p.b_gstride;
-        if (P::kScaled && p.ch_sb) p.ch_sb += (int64_t)spot.g * p.N;
-    } else {
-        tile_coords<false>(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-        m0 = tm * BM;
-        rows_m = min(p.M - m0, BM);
+        tiles = {p.offsets, p.G, p.M, lane, 0, 0, 0};
+        row_tiles = tiles.count();
     }
-    if constexpr (PLACE == PLACE_SUMS) {
-        // expert y's rows are the K elements of both operands (fewer than 2^31
-        // bytes of offsets per K step; the bases are 64-bit)
-        const int g = blockIdx.y, first = row_offset(p.offsets, g, p.rows);
-        p.K = p.krows = max(0, row_offset(p.offsets, g + 1, p.rows) - first);
-        p.A += (int64_t)first * p.lda;
-        p.B += (int64_t)first * p.ldb;
-        p.D += (int64_t)g * p.d_gstride;
-    }
-    const int n0 = tn * BNO;
-    const int rows_n = min(p.N - n0, BNO);
-    const int y = PLACE == PLACE_DENSE ? blockIdx.y : 0;
-    uint16_t *const d = y ? p.D2 : p.D;
+    auto place = [&](int t, Where &w) -> bool {
+        int tm, tn;
+        if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
+            if (t >= row_tiles * p.tiles_n) return false;
+            tile_coords<true>(t, row_tiles, p.tiles_n, tm, tn);
+            typename RaggedTiles<BM, PLACE == PLACE_REST>::Spot spot;
+            if (!tiles.find(tm, spot, false)) return false;
+            w = Where{spot.g, spot.m0, spot.rows, tn};
+        } else if constexpr (PLACE == PLACE_SUMS) {
+            if (t >= p.G * p.tiles_m * p.tiles_n) return false;
+            tile_coords<true>(t, p.G * p.tiles_m, p.tiles_n, tm, tn);
+            const int m0 = (tm % p.tiles_m) * BM;
+            w = Where{tm / p.tiles_m, m0, min(p.M - m0, BM), tn};
+        } else {
+            if (PERSIST && t >= p.tiles_m * p.tiles_n) return false;
+            tile_coords<false>(t, p.tiles_m, p.tiles_n, tm, tn);
+            w = Where{0, tm * BM, min(p.M - tm * BM, BM), tn};
+        }
+        return true;
+    };
+    Where now;
+    if (!place(blockIdx.x, now) && PERSIST) return;
+    const int y = PERSIST ? 0 : blockIdx.y;
     // this split's K steps: kb .. kb + nk - 1
     constexpr bool SPLIT = EPI == EPI_PARTIAL;
     const int kb = SPLIT ? (int)blockIdx.z * p.ksteps : 0;
-    const int nk = SPLIT ? min((p.K + KE - 1) / KE - kb, p.ksteps) : (p.K + KE - 1) / KE;
 
     // ---- copies ----
     // K-contiguous: copy qq fills ring rows 8 qq .. 8 qq + 7, lane l row l / 8,
@@ -160,40 +174,69 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     // Gated: copies 4 q, 4 q + 1 fill ring rows 32 q .. + 15 with rows 16 q ..
     // + 15 of p.B, 4 q + 2 and 4 q + 3 the next 16 with those of p.B2 (a second
     // descriptor).
-    uint32_t lo_a[CPA], lo_b[CPB];
+    // The tile being copied: operands, rows, K; set by `aim`.
+    uint32_t lo_a[CPA], lo_b[CPB], bytes_a, bytes_b, bytes_b1;
+    const uint8_t *a0, *b0, *b1;
+    uint16_t *d;
+    int m0, n0, rows_m, rows_n, K = p.K, krows = p.krows, nk;
+    const float *const expert_sb = P::kScaled ? p.ch_sb : nullptr;
+    auto aim = [&](const Where &w) {
+        m0 = w.m0;
+        rows_m = w.rows;
+        n0 = w.tn * BNO;
+        rows_n = min(p.N - n0, BNO);
+        const uint8_t *A = p.A + (int64_t)y * p.a_gstride, *B = p.B;
+        d = y ? p.D2 : p.D;
+        if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
+            if (PLACE == PLACE_REST) K = w.g < 0 ? 0 : p.K;        // (the empty sum)
+            B += (int64_t)max(w.g, 0) * p.b_gstride;
+            if (P::kScaled && expert_sb) p.ch_sb = expert_sb + (int64_t)w.g * p.N;
+        }
+        if constexpr (PLACE == PLACE_SUMS) {
+            // the expert's rows are the K elements of both operands
+            const int first = row_offset(p.offsets, w.g, p.rows);
+            K = krows = max(0, row_offset(p.offsets, w.g + 1, p.rows) - first);
+            A += (int64_t)first * p.lda;
+            B += (int64_t)first * p.ldb;
+            d += (int64_t)w.g * p.d_gstride;
+        }
 #pragma unroll
-    for (int i = 0; i < CPA; ++i) {
-        const int qq = wave * CPA + i;
-        lo_a[i] = TA ? strided_off(qq, BM, (rows_m + 7) & ~7, p.lda)
-                     : (uint32_t)(qq * 8 + (int)lr) * (uint32_t)p.lda + ((i & 1) ? kc1 : kc0);
-    }
+        for (int i = 0; i < CPA; ++i) {
+            const int qq = wave * CPA + i;
+            lo_a[i] = TA ? strided_off(qq, BM, (rows_m + 7) & ~7, p.lda)
+                         : (uint32_t)(qq * 8 + (int)lr) * (uint32_t)p.lda + ((i & 1) ? kc1 : kc0);
+        }
 #pragma unroll
-    for (int i = 0; i < CPB; ++i) {
-        const int qq = wave * CPB + i;
-        const int row = GATED ? (qq / 4) * 16 + (qq & 1) * 8 + (int)lr : qq * 8 + (int)lr;
-        lo_b[i] = TB ? strided_off(qq, BN, (rows_n + 7) & ~7, p.ldb)
-                     : (uint32_t)row * (uint32_t)(GATED && (i & 2) ? p.ldb2 : p.ldb) + ((i & 1) ? kc1 : kc0);
-    }
-    const uint8_t *const a0 = p.A + (int64_t)y * p.a_gstride + (TA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
-    const uint8_t *const b0 = p.B + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
-    // K-strided: rows of K steps from ksplit on; gated: the second matrix
-    const uint8_t *const b1 = p.B2 + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb2);
-    const uint32_t bytes_a = rows_bytes(rows_m, p.lda), bytes_b = rows_bytes(rows_n, p.ldb);
-    const uint32_t bytes_b1 = rows_bytes(rows_n, p.ldb2);
+        for (int i = 0; i < CPB; ++i) {
+            const int qq = wave * CPB + i;
+            const int row = GATED ? (qq / 4) * 16 + (qq & 1) * 8 + (int)lr : qq * 8 + (int)lr;
+            lo_b[i] = TB ? strided_off(qq, BN, (rows_n + 7) & ~7, p.ldb)
+                         : (uint32_t)row * (uint32_t)(GATED && (i & 2) ? p.ldb2 : p.ldb) + ((i & 1) ? kc1 : kc0);
+        }
+        a0 = A + (TA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
+        b0 = B + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
+        // K-strided: rows of K steps from ksplit on; gated: the second matrix
+        b1 = p.B2 + (TB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb2);
+        bytes_a = rows_bytes(rows_m, p.lda);
+        bytes_b = rows_bytes(rows_n, p.ldb);
+        bytes_b1 = rows_bytes(rows_n, p.ldb2);
+        nk = SPLIT ? min((K + KE - 1) / KE - kb, p.ksteps) : (K + KE - 1) / KE;
+    };
+    aim(now);
     v4i srdA, srdB, srdB1 = {0, 0, 0, 0};
     uint32_t lds_a = 0, lds_b = 0, ko0 = 0, ko1 = 0;
     auto set_step = [&](int kd) {                  // the copies of local step kd follow
         const int k = kb + kd;
         const bool in = kd < nk;
         if constexpr (TA) {
-            srdA = make_srd(a0 + (int64_t)k * KE * p.lda, in ? rows_bytes(min(KE, p.K - k * KE), p.lda) : 0u);
+            srdA = make_srd(a0 + (int64_t)k * KE * p.lda, in ? rows_bytes(min(KE, K - k * KE), p.lda) : 0u);
         } else {
             srdA = make_srd(a0 + (int64_t)k * BK, in ? bytes_a - (uint32_t)(k * BK) : 0u);
         }
         if constexpr (TB) {
             const bool late = PLACE == PLACE_DENSE && k >= p.ksplit;
             const int ks = late ? k - p.ksplit : k;
-            srdB = make_srd((late ? b1 : b0) + (int64_t)ks * KE * p.ldb, in ? rows_bytes(min(KE, p.krows - ks * KE), p.ldb) : 0u);
+            srdB = make_srd((late ? b1 : b0) + (int64_t)ks * KE * p.ldb, in ? rows_bytes(min(KE, krows - ks * KE), p.ldb) : 0u);
         } else {
             srdB = make_srd(b0 + (int64_t)k * BK, in ? bytes_b - (uint32_t)(k * BK) : 0u);
             if constexpr (GATED) srdB1 = make_srd(b1 + (int64_t)k * BK, in ? bytes_b1 - (uint32_t)(k * BK) : 0u);
@@ -202,7 +245,7 @@ __device__ __forceinline__ void tile_halves_body(P p) {
         lds_b = lds0 + (uint32_t)(kd % STAGES) * SLOT + (uint32_t)BM * BK + (uint32_t)(wave * CPB) * 1024u;
         // K-contiguous: lanes whose chunk starts at or past K
         if constexpr (TAIL) {
-            const int lim = ES * (p.K - k * KE);
+            const int lim = ES * (K - k * KE);
             ko0 = (int)kc0 < lim ? 0u : kOobOffset;
             ko1 = (int)kc1 < lim ? 0u : kOobOffset;
         }
@@ -245,10 +288,13 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     };
 
     Acc acc[FN][FM];
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = (Acc){0, 0, 0, 0};
+            for (int j = 0; j < FM; ++j) acc[i][j] = (Acc){0, 0, 0, 0};
+    };
+    clear();
 
     auto pin = [&] {
 #pragma unroll
@@ -298,33 +344,126 @@ __device__ __forceinline__ void tile_halves_body(P p) {
         });
     };
 
-    if constexpr (EPI == EPI_ACT) copy_tile_terms(p, smem + RING, lds0 + (uint32_t)RING, wave, lane, m0, rows_m, n0, rows_n);
+    // The copies ahead of a tile's first step: its terms (into slot `part`), STAGES steps.
+    auto begin = [&](int part) {
+        if constexpr (TERMS > 0)
+            copy_tile_terms(p, smem + RING + part * TERMS, lds0 + (uint32_t)(RING + part * TERMS), wave, lane, m0, rows_m, n0, rows_n);
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) {
-        set_step(s);
+        for (int s = 0; s < STAGES; ++s) {
+            set_step(s);
 #pragma unroll
-        for (int i = 0; i < CPW; ++i) issue_one(i);
-    }
-    vmcnt_wait<CPW * (STAGES - 1)>();              // this wave's part of step 0 has landed
-    __syncthreads();
+            for (int i = 0; i < CPW; ++i) issue_one(i);
+        }
+    };
+    auto sum = [&] {
+        __syncthreads();                           // everyone's part of step 0 has landed
 #pragma unroll
-    for (int q = 0; q < NFR; ++q) read_frag(f0b, f0a, smem, 0, q);
-    constexpr bool kPin = I8 || PLACE == PLACE_SUMS;
-    if constexpr (kPin) pin();
-    for (int kt = 0; kt < nk; ++kt) {
-        __builtin_amdgcn_sched_barrier(0);
-        step(kt);
+        for (int q = 0; q < NFR; ++q) read_frag(f0b, f0a, smem, 0, q);
+        // (pinned to AGPRs at the loop's exit: without this the 128-row builds
+        // carry the sums in VGPRs around the loop and copy them to AGPRs and
+        // back in every step.  Integer sums, and those of the persistent forms,
+        // need it at both ends of the loop's body as well: 450 copies beside
+        // the 128 matrix instructions of a step otherwise, and 4096 x 14336 x
+        // 4096 in 8-bit integers took 305 us.)
+        constexpr bool kPin = I8 || PERSIST;
         if constexpr (kPin) pin();
-    }
+        for (int kt = 0; kt < nk; ++kt) {
+            __builtin_amdgcn_sched_barrier(0);
+            step(kt);
+            if constexpr (kPin) pin();
+        }
+    };
+
+    begin(0);
+    vmcnt_wait<CPW * (STAGES - 1)>();              // this wave's part of step 0 has landed
+    if constexpr (PERSIST) {
+        // The direct epilogue, a wave by itself: 16 rows x 64 columns of its
+        // part at a time are rounded, laid out by rows in its own 2 KB of LDS
+        // (chunk c of row r at c ^ (r % 8)) and stored as whole 128-byte row
+        // segments, while the next tile's copies are under way.  Stores outside
+        // the matrix get an offset past the descriptor's end instead of a
+        // branch, so that their number is known to the wait for those copies.
+        constexpr int PASS_N = TN / 64, STORES = FM * PASS_N * 2;
+        static_assert(TN % 64 == 0 && CPW * (STAGES - 1) + STORES < 64, "stores in flight");
+        uint8_t *const st = smem + STAGE_AT + wave * STAGE;
+        const uint32_t ld2 = (uint32_t)p.ldd * 2u;
+        auto store = [&](uint16_t *out, int rows, int col0, const uint8_t *terms) {
+            // (the lane taken afresh: nothing of this is kept live across the loop)
+            const int el = lane_id_here(), r16 = el & 15, kg = el >> 4, er = el >> 3, ec = el & 7;
+            uint32_t put[4];
+    #pragma unroll
+            for (int i = 0; i < 4; ++i)
+                put[i] = (uint32_t)(r16 * 128 + (((i * 2 + (kg >> 1)) ^ (r16 & 7)) * 16) + (kg & 1) * 8);
+            const uint32_t get = (uint32_t)(er * 128 + ((ec ^ er) * 16));
+            const __amdgpu_buffer_rsrc_t to = make_rsrc(out, rows_bytes(rows, (int64_t)ld2));
+            const float *const tf = reinterpret_cast<const float *>(terms);
+            v4u held[2];
+            uint32_t at[2];
+            static_for<FM * PASS_N + 1>([&](auto pc) {
+                constexpr int pass = pc.value, j = pass / PASS_N, h = pass % PASS_N;
+                v4u v[2];
+                if constexpr (pass < FM * PASS_N) {
+                    const float sa = EPI == EPI_SCALED ? tf[wm * TM + j * 16 + r16] : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v4f z = sums_f32(acc[h * 4 + i][j]);
+                        if constexpr (EPI == EPI_SCALED) {
+                            const int c = wn * TN + (h * 4 + i) * 16 + kg * 4;
+                            const v4f sb = *reinterpret_cast<const v4f *>(tf + 256 + c), b = *reinterpret_cast<const v4f *>(tf + 512 + c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) z[e] = z[e] * sa * sb[e] + b[e];
+                        }
+                        *reinterpret_cast<v2u *>(st + put[i]) = pack_bf16x4(z[0], z[1], z[2], z[3]);
+                    }
+                    // (a wave's LDS accesses keep their order: the next pass may write behind these reads)
+                    v[0] = *reinterpret_cast<const v4u *>(st + get);
+                    v[1] = *reinterpret_cast<const v4u *>(st + get + 1024);
+                }
+                if constexpr (pass > 0) {
+                    __builtin_amdgcn_raw_buffer_store_b128(held[0], to, at[0], 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(held[1], to, at[1], 0, 0);
+                }
+                if constexpr (pass < FM * PASS_N) {
+                    const int col = wn * TN + h * 64 + ec * 8;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int row = wm * TM + j * 16 + q * 8 + er;
+                        at[q] = row < rows && col0 + col < p.N ? (uint32_t)row * ld2 + 2u * (uint32_t)col : kOobOffset;
+                        held[q] = v[q];
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        int t = blockIdx.x, part = 0;
+        for (;;) {
+            t += gridDim.x;
+            Where next;
+            const bool more = place(t, next);      // (its loads, if any, before the loop)
+            sum();
+            uint16_t *const out = d + (int64_t)m0 * p.ldd + n0;
+            const int rows = rows_m, col0 = n0;
+            vmcnt_wait<0>();                       // the copies past the last step (zeros)
+            // (No barrier: the slots refilled now were last read before the last
+            // step's first barrier, but for fragments that nobody uses.)
+            if (more) {
+                aim(next);
+                begin(part ^ 1);
+            }
+            // the last matrix instruction's result may be read: the pins above
+            // hide it from the compiler, which would have waited itself
+            asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+            pin();
+            store(out, rows, col0, smem + RING + part * TERMS);
+            if (!more) return;
+            part ^= 1;
+            clear();
+            vmcnt_wait<CPW * (STAGES - 1) + STORES>();   // this wave's part of step 0 has landed
+        }
+    } else {
+    sum();
     vmcnt_wait<0>();                               // drain the copies past the last step
     __syncthreads();                               // every wave's have landed; the ring is free
-
-    // (pinned to AGPRs at the loop's exit: without this the 128-row builds carry
-    // the sums in VGPRs around the loop and copy them to AGPRs and back in every
-    // step.  Integer sums, and those of the ragged weight gradients, need it at
-    // both ends of the loop's body as well: 450 copies beside the 128 matrix
-    // instructions of a step otherwise, and 4096 x 14336 x 4096 in 8-bit
-    // integers took 305 us.)
     pin();
 
     // ---- epilogue: register r of a block holds weight row 4 (l / 16) + r and
@@ -350,6 +489,7 @@ __device__ __forceinline__ void tile_halves_body(P p) {
                 }
                 __syncthreads();
             });
+    }
 }
 
 }  // namespace fp8g

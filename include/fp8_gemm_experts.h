@@ -25,7 +25,7 @@
  * outside 0 .. M count as the nearer end; where the offsets decrease, which of
  * the rows concerned are computed, and with which expert's weights, is not
  * defined, but nothing outside the matrices is read or written.  The host
- * never reads the offsets: the kernel is chosen from M / G.
+ * never reads the offsets: the kernel is chosen from M and G.
  *   B: expert g's [N x K] weights begin b_stride elements after those of
  *   expert g - 1 (b_stride >= (N - 1) ldb + K and aligned as ldb is).
  *   N % 8 == 0, G <= 65535.
@@ -44,7 +44,8 @@ extern "C" {
 /*
  * Ragged grouped product, BF16:
  *   D[r][n] = bf16_rne( sum_k A[r][k] B[g][n][k] )   for the rows r of expert g
- *   A [M][lda], D [M][ldd] BF16, 16-byte aligned.  Rows of no expert are
+ *   A [M][lda], D [M][ldd] BF16, 16-byte aligned; ldd at most (2^23 - 16) / 2,
+ *   as every output's stride here.  Rows of no expert are
  *   neither read from A nor written to D.  K = 0 writes zeros.
  * Few rows per expert take the few-token kernel (16, 32 or 64 weight rows per
  * workgroup, tiles of 16, 32 or 64 rows of one expert), more the LDS-tiled one
@@ -104,11 +105,11 @@ int int8_quantize_rows(const void *X, int64_t ldx, void *Q, int64_t ldq, float *
  * Kernel choice for a problem, without launching anything (host only).
  *   op: 0 = bf16_grouped_gemm_ragged, 1 = int8_grouped_gemm_ragged, 2 = its
  *   BF16 token gradient (m x k, reduced over n), 3 = the weight gradients (n x
- *   k each, reduced over the expert's rows), 4 = int8_gemm_nt_fused (groups
- *   is not used).
- * Fills the plan of fp8_gemm.h as fp8_gemm_fused_plan does; workgroups is the
- * launch's number, of which those past the tiles that the offsets give leave at
- * once.
+ *   k each, reduced over the expert's rows), 4 = int8_gemm_nt_fused without
+ *   activation and residual (groups is not used).
+ * Fills the plan of fp8_gemm.h as fp8_gemm_fused_plan does; workgroups counts
+ * as many tiles as any offsets can need (the tiled kernels run them on at most
+ * 256 persistent workgroups).
  */
 int fp8_gemm_experts_plan(int op, int m, int n, int k, int groups, fp8g_plan *out);
 

@@ -149,6 +149,22 @@ def test_only_these_builds_exist():
         assert set(builds(op)) == {b[1:] for b in BUILDS if b[0] == kind}, kind
 
 
+def test_persistent_rounds(f):
+    """More tiles than workgroups, empty experts among them: the copies ahead of the next tile, one K step and many."""
+    counts = [0, 1, 700, 0, 129, 1500, 3, 0, 2000, 256]
+    for N, K in ((8200, 16), (8200, 208)):
+        assert f.experts_plan(0, 4700, N, K, 10).workgroups > 512
+        forward(f, "bf16", counts, N, K, 50, 61)
+        forward(f, "int8", counts, N, K, 50, 61)
+    a = E.with_nan_outside(rand(1, 4700, 4104), counts, 50)
+    backward_check(f, a, rand(2, 10, 1032, 4104, std=0.25), offsets_of(counts, 50), counts, 50)
+    # more than 64 experts, whose offsets are read anew for every tile
+    counts = E.divide(9000, 150, 5)
+    forward(f, "bf16", counts, 2056, 64, 7, 9)
+    a = rand(1, 9000, 2056)
+    backward_check(f, a, rand(2, 150, 136, 2056, std=0.25), offsets_of(counts), counts, 0)
+
+
 # ---- as they are used
 def test_strided(f):
     """Rows and experts apart in memory, NaN between them; outputs as columns of a wider buffer."""

@@ -22,7 +22,7 @@ def check(f, M, N, K, i, res=None, out=None):  # noqa: F811
     if i % 3 == 1:
         sa = sa * 1e-3
     bias = rand(3, N, dtype=torch.float32) if i % 2 else None
-    if res is None and i != 2:
+    if res is None and i not in (2, 5, 10):                # (5, 10: no activation either, the direct epilogue)
         res = rand(4, M, N)
     kept = None if res is None else res.clone()
     name = F.ACTS[i % 5]
@@ -47,37 +47,47 @@ SHAPES = [(1, 1, 16), (1, 130, 272), (5, 33, 400), (16, 64, 128), (17, 100, 144)
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_shapes(f, M, N, K):  # noqa: F811
-    for i in range(5):
+    for i in (0, 1, 2, 3, 4, 5, 10):
         check(f, M, N, K, i)
 
 
 @functools.lru_cache(None)
-def builds():
+def builds(direct):
+    """{build: the cheapest of the candidate sizes that takes it}; direct: whole chunks of columns and neither activation
+    nor residual."""
     import fp8_gemm_amd as f
     best = {}
     for m in (1, 3, 17, 40, 65, 130, 300, 700, 1000, 2000, 2100, 3000):
-        for n in (8, 40, 136, 515, 1032, 2056, 4104, 8200, 14336):
+        for n in (8, 40, 136, 520, 1032, 2056, 4104, 8200, 14336):
             for k in (1152, 1168, 2048):
-                p = f.experts_plan(4, m, n, k)
+                p = f.experts_plan(4, m, n if direct else n - 3, k)
                 key = (p.variant, p.tile_m, p.tile_n, p.variant != 4 and k % 128 != 0)
                 if m * n * k < best.get(key, (1e300,))[0]:
-                    best[key] = m * n * k, (m, n, k)
+                    best[key] = m * n * k, (m, n if direct else n - 3, k)
     return {k: v[1] for k, v in best.items()}
 
 
 BUILDS = [(*t, tail) for t in TILES for tail in (False, True)] + [(*t, False) for t in FEW]
 
 
+@pytest.mark.parametrize("direct", [True, False], ids=["direct", "staged"])
 @pytest.mark.parametrize("build", BUILDS, ids=lambda b: "-".join(map(str, b)))
-def test_every_build(f, build):  # noqa: F811
-    found = builds()
+def test_every_build(f, build, direct):  # noqa: F811
+    found = builds(direct)
     assert build in found, sorted(found)
-    check(f, *found[build], 3)
-    check(f, *found[build], 2)
+    for i in (5, 10) if direct else (3, 2):
+        check(f, *found[build], i)
 
 
 def test_only_these_builds_exist():
-    assert set(builds()) == set(BUILDS)
+    assert set(builds(True)) == set(builds(False)) == set(BUILDS)
+
+
+def test_persistent_rounds(f):  # noqa: F811
+    """More tiles than workgroups: the copies ahead of the next tile, with and without a K tail, one step and many."""
+    for M, N, K in ((4100, 8200, 16), (4100, 8200, 144), (4100, 8200, 400), (9000, 5000, 16), (20000, 1032, 272)):
+        assert f.experts_plan(4, M, N, K).workgroups > 300
+        check(f, M, N, K, 5)
 
 
 @pytest.mark.parametrize("M", [1, 40, 200, 2100])
