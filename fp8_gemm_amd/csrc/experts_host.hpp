@@ -170,8 +170,8 @@ int check_grid(int64_t workgroups) {
     return FP8G_OK;
 }
 
-// Persistent workgroups: one per CU.
-int64_t persistent_grid(int64_t tiles) { return tiles < 256 ? tiles : 256; }
+// Persistent workgroups: one per CU (few tiles are cut in two).
+int64_t persistent_grid(int64_t tiles) { return 2 * tiles < 256 ? 2 * tiles : 256; }
 
 template <int BM, int BN, int STAGES, int FMT, bool TB, int PLACE, int EPI>
 int launch_rows_shape(const FusedArgs &a, const int32_t *offsets, hipStream_t s) {

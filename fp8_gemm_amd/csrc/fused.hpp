@@ -68,13 +68,14 @@ struct Int8Params : FusedParams<E, true> {
 // Over ragged groups of rows (ragged.hpp): expert g's weights begin b_gstride
 // bytes after those of expert g - 1, its channel scales N floats, its weight
 // gradient d_gstride elements.  rows: PLACE_SUMS, the number of token rows (M
-// and N are the gradient's).  Scales come with 8-bit integers only.
+// and N are the gradient's); stream: its stores bypass the caches.  Scales
+// come with 8-bit integers only.
 template <int E, bool SCALED, int PLACE>
 struct RaggedParams : FusedParams<E, SCALED> {
     static constexpr int kPlace = PLACE;
     static constexpr bool kIntSums = SCALED;
     const int32_t *offsets;
-    int rows;
+    int rows, stream;
 };
 
 // ---------------------------------------------------------------------------
@@ -272,9 +273,12 @@ __device__ __forceinline__ void copy_tile_terms(const P &p, uint8_t *terms, uint
     constexpr bool GATED = P::kEpilogue == EPI_GATED;
     float *const own = reinterpret_cast<float *>(terms) + wave * 64 + lane;
     auto copy = [&](const float *src, int step, int first, int count, int idx, int at, float absent) {
+        // (the persistent kernels are short of scalar registers: the compiler
+        // would keep the LDS address in a vector register, which M0 cannot take)
+        auto address = [](uint32_t a) { return P::kEpilogue == EPI_SCALED ? (uint32_t)__builtin_amdgcn_readfirstlane((int)a) : a; };
         if (src)
             dma4(make_srd(src + (int64_t)first * step, step ? rows_bytes(count, 4) : 4u),
-                 idx < count ? 4u * (uint32_t)(idx * step) : kOobOffset, lds + (uint32_t)(at + wave * 64) * 4u);
+                 idx < count ? 4u * (uint32_t)(idx * step) : kOobOffset, address(lds + (uint32_t)(at + wave * 64) * 4u));
         else
             own[at] = absent;
     };

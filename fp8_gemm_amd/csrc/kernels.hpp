@@ -1653,8 +1653,9 @@ __device__ __forceinline__ void decode_body(P p) {
     int tm0 = 0, rows_t = 0;
     if constexpr (RAGGED) {
         // 16 CB rows of one expert, times its weights
-        RaggedTiles<16 * CB, false> tiles{p.offsets, p.G, p.M, lane, 0, 0, 0};
-        typename RaggedTiles<16 * CB, false>::Spot spot;
+        using Tiles = RaggedTiles<16 * CB, false>;
+        Tiles tiles{p.offsets, p.G, p.M, lane, 0, 0, 0};
+        typename Tiles::Spot spot;
         if (!tiles.find((int)blockIdx.y, spot, true)) return;
         tm0 = spot.m0;
         rows_t = spot.rows;

@@ -58,7 +58,13 @@ namespace fp8g {
 // CU, each on tiles blockIdx.x, + gridDim.x, ..., so that the number of tiles
 // need not be known to the host.  A tile's first copies go out before the
 // tile before it is written, which hides their way from memory, the launch and
-// the offsets behind the epilogue.
+// the offsets behind the epilogue.  Tiles of at most BM / 2 rows (an expert's
+// last rows, the cut tiles of the last round) run a step of half the matrix
+// instructions, which takes about 0.7 of a whole one's time: 4096 x 14336 x 4096
+// in 8-bit integers, 3.5 rounds, 194 -> 174 us.  They stay in the order of
+// the rows: moved behind all whole tiles, for a balanced end, each expert's
+// weights came from memory twice, 8 experts of 14336 x 4096 over 8192 rows 795
+// against 757 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int strided_key(int k) { return 2 * (k & 3) + ((k >> 3) & 1); }
 
@@ -120,30 +126,46 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     struct Where {
         int g, m0, rows, tn;                       // expert, first row and rows, column of tiles
     };
-    RaggedTiles<BM, PLACE == PLACE_REST> tiles = {};
-    int row_tiles = 0;
-    if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
-        tiles = {p.offsets, p.G, p.M, lane, 0, 0, 0};
-        row_tiles = tiles.count();
+    // Persistent: whole tiles in rounds of one per workgroup, and if the last
+    // round has work for at most half of them, its `cut` tiles in two halves
+    // each, by rows.
+    using Tiles = RaggedTiles<BM, PLACE == PLACE_REST>;
+    Tiles tiles = {};
+    int row_tiles = 0, whole = 0, cut = 0;
+    if constexpr (PERSIST) {
+        if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
+            tiles = Tiles{p.offsets, p.G, p.M, lane, 0, 0, 0};
+            row_tiles = tiles.count();
+        } else {
+            row_tiles = PLACE == PLACE_SUMS ? p.G * p.tiles_m : p.tiles_m;
+        }
+        whole = row_tiles * p.tiles_n;
+        const int left = whole % (int)gridDim.x;
+        if (2 * left <= (int)gridDim.x) cut = left;
+        whole -= cut;
     }
     auto place = [&](int t, Where &w) -> bool {
         int tm, tn;
-        if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
-            if (t >= row_tiles * p.tiles_n) return false;
-            tile_coords<true>(t, row_tiles, p.tiles_n, tm, tn);
-            typename RaggedTiles<BM, PLACE == PLACE_REST>::Spot spot;
-            if (!tiles.find(tm, spot, false)) return false;
-            w = Where{spot.g, spot.m0, spot.rows, tn};
-        } else if constexpr (PLACE == PLACE_SUMS) {
-            if (t >= p.G * p.tiles_m * p.tiles_n) return false;
-            tile_coords<true>(t, p.G * p.tiles_m, p.tiles_n, tm, tn);
-            const int m0 = (tm % p.tiles_m) * BM;
-            w = Where{tm / p.tiles_m, m0, min(p.M - m0, BM), tn};
-        } else {
-            if (PERSIST && t >= p.tiles_m * p.tiles_n) return false;
+        if constexpr (!PERSIST) {
             tile_coords<false>(t, p.tiles_m, p.tiles_n, tm, tn);
             w = Where{0, tm * BM, min(p.M - tm * BM, BM), tn};
+            return true;
         }
+        const int u = t - whole;                   // >= 0: half u / cut of a tile
+        if (u >= 2 * cut) return false;
+        // (the dense order keeps each XCD on its own part of the matrix, the
+        // other one all of them on the same experts)
+        tile_coords<PLACE != PLACE_DENSE>(u < cut ? t : t - cut, row_tiles, p.tiles_n, tm, tn);
+        if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
+            typename Tiles::Spot spot;
+            if (!tiles.find(tm, spot, false)) return false;
+            w = Where{spot.g, spot.m0, spot.rows, tn};
+        } else {
+            const int m0 = (PLACE == PLACE_SUMS ? tm % p.tiles_m : tm) * BM;
+            w = Where{PLACE == PLACE_SUMS ? tm / p.tiles_m : 0, m0, min(p.M - m0, BM), tn};
+        }
+        if (u >= cut) w.m0 += BM / 2;
+        if (u >= 0) w.rows = u < cut ? min(w.rows, BM / 2) : max(0, w.rows - BM / 2);
         return true;
     };
     Where now;
@@ -181,9 +203,12 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     int m0, n0, rows_m, rows_n, K = p.K, krows = p.krows, nk;
     const float *const expert_sb = P::kScaled ? p.ch_sb : nullptr;
     auto aim = [&](const Where &w) {
-        m0 = w.m0;
-        rows_m = w.rows;
-        n0 = w.tn * BNO;
+        // (uniform, which the compiler does not see through the persistent
+        // loop; the branches and the copies' LDS addresses depend on it)
+        auto uniform = [](int v) { return PERSIST ? __builtin_amdgcn_readfirstlane(v) : v; };
+        m0 = uniform(w.m0);
+        rows_m = uniform(w.rows);
+        n0 = uniform(w.tn) * BNO;
         rows_n = min(p.N - n0, BNO);
         const uint8_t *A = p.A + (int64_t)y * p.a_gstride, *B = p.B;
         d = y ? p.D2 : p.D;
@@ -221,6 +246,9 @@ __device__ __forceinline__ void tile_halves_body(P p) {
         bytes_b = rows_bytes(rows_n, p.ldb);
         bytes_b1 = rows_bytes(rows_n, p.ldb2);
         nk = SPLIT ? min((K + KE - 1) / KE - kb, p.ksteps) : (K + KE - 1) / KE;
+        // the second half of a cut tile may have no rows: no steps then, whose
+        // descriptors would count bytes down from 0
+        if (PERSIST && rows_m <= 0) nk = 0;
     };
     aim(now);
     v4i srdA, srdB, srdB1 = {0, 0, 0, 0};
@@ -257,6 +285,11 @@ __device__ __forceinline__ void tile_halves_body(P p) {
                       lds_b + (uint32_t)(i - CPA) * 1024u);
     };
 
+    // Row blocks of 16 of the token side: the wave's part in one piece, or
+    // (persistent) every second one, so that a tile's rows, however few, are
+    // shared by both waves.
+    auto row_block = [&](int f) { return PERSIST ? 2 * f + wm : wm * FM + f; };
+
     // ---- fragments: lane l carries row l % 16 of a 16-row block and, of K
     // half h, bytes 16 (l / 16) .. + 15
     const int r16 = lane & 15, kg = lane >> 4;
@@ -268,7 +301,7 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     uint32_t to_a[FM], to_b[FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f)
-        to_a[f] = (uint32_t)(trow * BM * 2 + ((wm * FM + f) ^ strided_key(trow)) * 32 + (lane & 3) * 8);
+        to_a[f] = (uint32_t)(trow * BM * 2 + (row_block(f) ^ strided_key(trow)) * 32 + (lane & 3) * 8);
 #pragma unroll
     for (int f = 0; f < FN; ++f)
         to_b[f] = (uint32_t)(trow * BN * 2 + ((wn * FN + f) ^ strided_key(trow)) * 32 + (lane & 3) * 8);
@@ -284,39 +317,40 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     // fragment q of K half h: weight block q < FN, else token block q - FN
     auto read_frag = [&](v4u (&bf)[FN], v4u (&af)[FM], const uint8_t *slot, int h, int q) {
         if (q < FN) bf[q] = frag(int_c<TB>{}, slot + BM * BK + (TB ? 0 : (wn * TN + q * 16) * BK), to_b[q], BN * 2, h);
-        else af[q - FN] = frag(int_c<TA>{}, slot + (TA ? 0 : (wm * TM + (q - FN) * 16) * BK), to_a[q - FN], BM * 2, h);
+        else af[q - FN] = frag(int_c<TA>{}, slot + (TA ? 0 : row_block(q - FN) * 16 * BK), to_a[q - FN], BM * 2, h);
     };
 
-    Acc acc[FN][FM];
-    auto clear = [&] {
+    // The sums of FN x FMV blocks: FMV = FM, or (half tiles) FM / 2.
+    auto clear = [&](auto &acc) {
+        constexpr int FMV = sizeof(acc[0]) / sizeof(Acc);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] = (Acc){0, 0, 0, 0};
+            for (int j = 0; j < FMV; ++j) acc[i][j] = (Acc){0, 0, 0, 0};
     };
-    clear();
-
-    auto pin = [&] {
+    auto pin = [&](auto &acc) {
+        constexpr int FMV = sizeof(acc[0]) / sizeof(Acc);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+            for (int j = 0; j < FMV; ++j) asm volatile("" : "+a"(acc[i][j]));
     };
 
     // One K step (see above).  (Unrolled by the template: the loop pragma gave
     // up on K-strided operands.)
-    constexpr int NMF = FN * FM, NFR = FN + FM, T = 2 * NMF;
-    constexpr int kRead1 = T / 4, kBarA = 17 * T / 64, kCopyTo = T, kBarB = 5 * T / 8;
-    static_assert(kRead1 <= kBarA && kBarA < NMF && kBarB >= NMF && kCopyTo <= T, "schedule");
-    // copies out at barrier B: those issued from barrier A on
-    constexpr int kIssued = ((kBarB - kBarA) * CPW) / (kCopyTo - kBarA);
-    static_assert(CPW * (STAGES - 2) + kIssued < 64, "copies in flight");
     v4u f0b[FN], f0a[FM], f1b[FN], f1a[FM];
-    auto step = [&](int kt) {
+    auto step = [&](auto &acc, int kt) {
+        constexpr int FMV = sizeof(acc[0]) / sizeof(Acc);
+        constexpr int NMF = FN * FMV, NFR = FN + FMV, T = 2 * NMF;
+        constexpr int kRead1 = T / 4, kBarA = 17 * T / 64, kCopyTo = T, kBarB = 5 * T / 8;
+        static_assert(kRead1 <= kBarA && kBarA < NMF && kBarB >= NMF && kCopyTo <= T, "schedule");
+        // copies out at barrier B: those issued from barrier A on
+        constexpr int kIssued = ((kBarB - kBarA) * CPW) / (kCopyTo - kBarA);
+        static_assert(CPW * (STAGES - 2) + kIssued < 64, "copies in flight");
         const uint8_t *cur = smem + (kt % STAGES) * SLOT;
         const uint8_t *nxt = smem + ((kt + 1) % STAGES) * SLOT;
         static_for<T>([&](auto tc) {
-            constexpr int t = tc.value, i = (t % NMF) / FM, j = (t % NMF) % FM;
+            constexpr int t = tc.value, i = (t % NMF) / FMV, j = (t % NMF) % FMV;
             if constexpr (t == kBarA) {
                 __syncthreads();                   // step kt's slot is no longer read
                 set_step(kt + STAGES);
@@ -355,10 +389,11 @@ __device__ __forceinline__ void tile_halves_body(P p) {
             for (int i = 0; i < CPW; ++i) issue_one(i);
         }
     };
-    auto sum = [&] {
+    auto sum = [&](auto &acc) {
+        constexpr int FMV = sizeof(acc[0]) / sizeof(Acc);
         __syncthreads();                           // everyone's part of step 0 has landed
 #pragma unroll
-        for (int q = 0; q < NFR; ++q) read_frag(f0b, f0a, smem, 0, q);
+        for (int q = 0; q < FN + FMV; ++q) read_frag(f0b, f0a, smem, 0, q);
         // (pinned to AGPRs at the loop's exit: without this the 128-row builds
         // carry the sums in VGPRs around the loop and copy them to AGPRs and
         // back in every step.  Integer sums, and those of the persistent forms,
@@ -366,16 +401,15 @@ __device__ __forceinline__ void tile_halves_body(P p) {
         // the 128 matrix instructions of a step otherwise, and 4096 x 14336 x
         // 4096 in 8-bit integers took 305 us.)
         constexpr bool kPin = I8 || PERSIST;
-        if constexpr (kPin) pin();
+        if constexpr (kPin) pin(acc);
         for (int kt = 0; kt < nk; ++kt) {
             __builtin_amdgcn_sched_barrier(0);
-            step(kt);
-            if constexpr (kPin) pin();
+            step(acc, kt);
+            if constexpr (kPin) pin(acc);
         }
     };
 
     begin(0);
-    vmcnt_wait<CPW * (STAGES - 1)>();              // this wave's part of step 0 has landed
     if constexpr (PERSIST) {
         // The direct epilogue, a wave by itself: 16 rows x 64 columns of its
         // part at a time are rounded, laid out by rows in its own 2 KB of LDS
@@ -383,15 +417,17 @@ __device__ __forceinline__ void tile_halves_body(P p) {
         // segments, while the next tile's copies are under way.  Stores outside
         // the matrix get an offset past the descriptor's end instead of a
         // branch, so that their number is known to the wait for those copies.
-        constexpr int PASS_N = TN / 64, STORES = FM * PASS_N * 2;
+        constexpr int PASS_N = TN / 64;
+        constexpr int STORES = FM * PASS_N * 2;    // of a wave (half tiles: half of them)
         static_assert(TN % 64 == 0 && CPW * (STAGES - 1) + STORES < 64, "stores in flight");
         uint8_t *const st = smem + STAGE_AT + wave * STAGE;
         const uint32_t ld2 = (uint32_t)p.ldd * 2u;
-        auto store = [&](uint16_t *out, int rows, int col0, const uint8_t *terms) {
+        auto store = [&](const auto &acc, uint16_t *out, int rows, int col0, const uint8_t *terms) {
+            constexpr int PASSES = sizeof(acc[0]) / sizeof(Acc) * PASS_N;
             // (the lane taken afresh: nothing of this is kept live across the loop)
             const int el = lane_id_here(), r16 = el & 15, kg = el >> 4, er = el >> 3, ec = el & 7;
             uint32_t put[4];
-    #pragma unroll
+#pragma unroll
             for (int i = 0; i < 4; ++i)
                 put[i] = (uint32_t)(r16 * 128 + (((i * 2 + (kg >> 1)) ^ (r16 & 7)) * 16) + (kg & 1) * 8);
             const uint32_t get = (uint32_t)(er * 128 + ((ec ^ er) * 16));
@@ -399,11 +435,11 @@ __device__ __forceinline__ void tile_halves_body(P p) {
             const float *const tf = reinterpret_cast<const float *>(terms);
             v4u held[2];
             uint32_t at[2];
-            static_for<FM * PASS_N + 1>([&](auto pc) {
+            static_for<PASSES + 1>([&](auto pc) {
                 constexpr int pass = pc.value, j = pass / PASS_N, h = pass % PASS_N;
                 v4u v[2];
-                if constexpr (pass < FM * PASS_N) {
-                    const float sa = EPI == EPI_SCALED ? tf[wm * TM + j * 16 + r16] : 1.0f;
+                if constexpr (pass < PASSES) {
+                    const float sa = EPI == EPI_SCALED ? tf[row_block(j) * 16 + r16] : 1.0f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         v4f z = sums_f32(acc[h * 4 + i][j]);
@@ -420,14 +456,21 @@ __device__ __forceinline__ void tile_halves_body(P p) {
                     v[1] = *reinterpret_cast<const v4u *>(st + get + 1024);
                 }
                 if constexpr (pass > 0) {
-                    __builtin_amdgcn_raw_buffer_store_b128(held[0], to, at[0], 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b128(held[1], to, at[1], 0, 0);
+                    bool stream = false;
+                    if constexpr (PLACE == PLACE_SUMS) stream = p.stream;
+                    if (stream) {                  // (cache bit 2: nontemporal)
+                        __builtin_amdgcn_raw_buffer_store_b128(held[0], to, at[0], 0, 2);
+                        __builtin_amdgcn_raw_buffer_store_b128(held[1], to, at[1], 0, 2);
+                    } else {
+                        __builtin_amdgcn_raw_buffer_store_b128(held[0], to, at[0], 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(held[1], to, at[1], 0, 0);
+                    }
                 }
-                if constexpr (pass < FM * PASS_N) {
+                if constexpr (pass < PASSES) {
                     const int col = wn * TN + h * 64 + ec * 8;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const int row = wm * TM + j * 16 + q * 8 + er;
+                        const int row = row_block(j) * 16 + q * 8 + er;
                         at[q] = row < rows && col0 + col < p.N ? (uint32_t)row * ld2 + 2u * (uint32_t)col : kOobOffset;
                         held[q] = v[q];
                     }
@@ -435,12 +478,21 @@ __device__ __forceinline__ void tile_halves_body(P p) {
                 __builtin_amdgcn_sched_barrier(0);
             });
         };
-        int t = blockIdx.x, part = 0;
-        for (;;) {
+        int t = blockIdx.x, part = 0, stores = 0;  // stores issued behind the copies of the tile at hand
+        // One tile (each kind with registers of its own for the sums: shared by
+        // both loops they were spilled); true: another one is under way.
+        auto tile = [&](auto fmv) -> bool {
+            constexpr int FMV = fmv.value;
+            Acc acc[FN][FMV];
+            clear(acc);
+            // this wave's part of step 0 has landed
+            if (stores == 0) vmcnt_wait<CPW * (STAGES - 1)>();
+            else if (stores == 1) vmcnt_wait<CPW * (STAGES - 1) + STORES / 2>();
+            else vmcnt_wait<CPW * (STAGES - 1) + STORES>();
             t += gridDim.x;
             Where next;
-            const bool more = place(t, next);      // (its loads, if any, before the loop)
-            sum();
+            const bool more = __builtin_amdgcn_readfirstlane(place(t, next));   // (its loads, if any, before the loop)
+            sum(acc);
             uint16_t *const out = d + (int64_t)m0 * p.ldd + n0;
             const int rows = rows_m, col0 = n0;
             vmcnt_wait<0>();                       // the copies past the last step (zeros)
@@ -453,18 +505,21 @@ __device__ __forceinline__ void tile_halves_body(P p) {
             // the last matrix instruction's result may be read: the pins above
             // hide it from the compiler, which would have waited itself
             asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
-            pin();
-            store(out, rows, col0, smem + RING + part * TERMS);
-            if (!more) return;
+            pin(acc);
+            store(acc, out, rows, col0, smem + RING + part * TERMS);
             part ^= 1;
-            clear();
-            vmcnt_wait<CPW * (STAGES - 1) + STORES>();   // this wave's part of step 0 has landed
-        }
+            stores = FMV == FM ? 2 : 1;
+            return more;
+        };
+        while (rows_m <= BM / 2 ? tile(int_c<FM / 2>{}) : tile(int_c<FM>{})) {}
     } else {
-    sum();
+    Acc acc[FN][FM];
+    clear(acc);
+    vmcnt_wait<CPW * (STAGES - 1)>();              // this wave's part of step 0 has landed
+    sum(acc);
     vmcnt_wait<0>();                               // drain the copies past the last step
     __syncthreads();                               // every wave's have landed; the ring is free
-    pin();
+    pin(acc);
 
     // ---- epilogue: register r of a block holds weight row 4 (l / 16) + r and
     // token l % 16

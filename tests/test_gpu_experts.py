@@ -165,6 +165,16 @@ def test_persistent_rounds(f):
     backward_check(f, a, rand(2, 150, 136, 2056, std=0.25), offsets_of(counts), counts, 0)
 
 
+def test_gradients_past_the_caches(f):
+    """Weight gradients above 256 MB, whose stores bypass the caches; rows and columns that end inside a tile."""
+    counts, N, K = [0, 150, 1, 129, 20, 0, 64, 3, 5], 4104, 4088
+    a = E.with_nan_outside(rand(1, sum(counts) + 9, K), counts, 4)
+    b = torch.zeros(9, N, K, dtype=BF, device=DEV)
+    b[:, ::37] = rand(2, 9, (N + 36) // 37, K)
+    assert b.numel() * 2 > 256 << 20
+    backward_check(f, a, b, offsets_of(counts, 4), counts, 4)
+
+
 # ---- as they are used
 def test_strided(f):
     """Rows and experts apart in memory, NaN between them; outputs as columns of a wider buffer."""
