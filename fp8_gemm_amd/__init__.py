@@ -806,10 +806,9 @@ def experts_plan(op: int, m: int, n: int, k: int, groups: int = 1) -> Plan:
     return out
 
 
-def _int8_only(tt, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != tt.i8:
-            raise TypeError(f"{name} must be int8, got {t.dtype}")
+def _int8_only(tt, a, b):
+    if a.dtype is not tt.i8 or b.dtype is not tt.i8:
+        raise TypeError(f"a and b must be int8, got {a.dtype} and {b.dtype}")
 
 
 def _ragged(tt, a, b, offsets):
@@ -892,7 +891,7 @@ def grouped_gemm_ragged_int8(a, b, offsets, scale_a=None, scale_b=None, out=None
     K % 16 == 0 and K <= 131056, N % 8 == 0.
     """
     tt = _tt()
-    _int8_only(tt, a=a, b=b)
+    _int8_only(tt, a, b)
     M, G, N, K = _ragged(tt, a, b, offsets)
     index = _device(a, b, offsets, scale_a, scale_b)
     lda = _operand(a, "a", M, K, 16)
@@ -914,7 +913,7 @@ def gemm_nt_int8(a, b, scale_a=None, scale_b=None, bias=None, activation="none",
     sums are exact: K % 16 == 0 and K <= 131056.
     """
     tt = _tt()
-    _int8_only(tt, a=a, b=b)
+    _int8_only(tt, a, b)
     M, N, K = _matrices(a, b, "b")
     index = _device(a, b, scale_a, scale_b, bias, residual)
     lda, ldb = _operand(a, "a", M, K, 16), _operand(b, "b", N, K, 16)
@@ -940,19 +939,24 @@ def quantize_rows_int8(x, codes=None, scales=None):
     K % 16 == 0.
     """
     tt = _tt()
-    _bf16_only(tt, x=x)
-    if x.dim() != 2:
-        raise ValueError(f"x must be a [M, K] tensor, got {list(x.shape)}")
-    M, K = x.shape
+    if x.dtype is not tt.bf16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be a [M, K] tensor, got {list(shape)}")
+    M, K = shape
     index = _device(x, codes, scales)
     ldx = _operand(x, "x", M, K, 16)
+    device = x.device
     if codes is None:
         ldq = (K + 15) // 16 * 16
-        codes = tt.empty((M, K), dtype=tt.i8, device=x.device)
+        codes = tt.empty(shape, dtype=tt.i8, device=device)
     else:
         ldq = _rows(codes, "codes", M, K, tt.i8)
+        if M == 1:
+            ldq = (K + 15) // 16 * 16              # (never stepped over)
     if scales is None:
-        scales = tt.empty(M, dtype=tt.f32, device=x.device)
+        scales = tt.empty(M, dtype=tt.f32, device=device)
     elif scales.dtype != tt.f32 or tuple(scales.shape) != (M,) or not scales.is_contiguous():
         raise ValueError(f"scales must be a contiguous float32 tensor with {M} elements")
     _call(tt, index, load_library().int8_quantize_rows, x.data_ptr(), ldx, codes.data_ptr(), ldq, scales.data_ptr(), M, K)

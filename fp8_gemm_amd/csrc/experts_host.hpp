@@ -64,27 +64,27 @@ int64_t tiles_bound(int64_t M, int64_t segments, int rows) {
 // whole tiles alone).
 //
 // The constants (us; the persistent kernels: launch, and per round of 256
-// workgroups a fixed part and the K steps) are fitted to 3047 measured cases,
-// every class each: 2 .. 160 experts, 1 .. 65536 rows divided unevenly, N 32 ..
-// 14336, K 64 .. 8192, the weights read from memory.  On average the choice
-// takes longer than the fastest class by 3.1% (BF16), 1.9% (8-bit integers),
-// 0.7% (token gradients) and 0.8% (weight gradients); with the dense products'
-// constants it was 6.1, 6.3, 1.0 and 5.8%.  Most of what is left are products of
-// few columns below 15 us, where the number of rows of the largest expert
-// matters, which the host does not know: at worst 2.1 times (BF16 2060 rows
-// of 41 experts, 56 x 288: 13.7 against 6.5 us) and 1.65 times (integers,
-// 12264 rows of 101 experts, 160 x 6000: 74 against 45 us).
+// workgroups a fixed part and the K steps, a last round of at most 128 tiles
+// counting 0.7) are fitted to 2555 measured cases, every class each: 2 .. 160
+// experts, 1 .. 65536 rows divided unevenly, N 32 .. 14336, K 64 .. 8192, the
+// weights read from memory.  On average the choice takes longer than the fastest
+// class by 3.4% (BF16), 2.0% (8-bit integers), 0.7% (token gradients), 1.3%
+// (weight gradients) and 0.1% (dense integers).  Most of what is left are
+// products of few columns, where the number of rows of the largest experts
+// matters, which the host does not know: at worst 1.8 times (BF16 1086 rows of
+// 7 experts, 224 x 7936: 41 against 22 us) and 1.7 times (integers, 5305 rows of
+// 57 experts, 152 x 4736: 39 against 23 us).
 // ---------------------------------------------------------------------------
 enum RaggedOp { R_BF16, R_INT8, R_TOKEN_GRAD, R_WEIGHT_GRAD };
 
-constexpr ClassCost kRaggedCost[4][3] = {{{1.7, 2.6, 0.343, 0.244}, {1.1, 4.0, 0.613, 0.408}, {1.2, 5.5, 0.949, 0.422}},
-                                         {{3.2, 3.6, 0.332, 0.217}, {3.2, 5.5, 0.584, 0.345}, {2.1, 8.4, 0.977, 0.395}},
-                                         {{2.4, 2.7, 0.380, 0.201}, {2.1, 4.1, 0.808, 0.185}, {2.4, 5.1, 1.006, 0.336}},
-                                         {{3.4, 2.3, 0.488, 0.148}, {4.0, 3.1, 1.082, 0.132}, {3.1, 4.5, 1.385, 0.360}}};
+constexpr ClassCost kRaggedCost[4][3] = {{{1.8, 2.5, 0.385, 0.233}, {1.4, 4.0, 0.640, 0.331}, {1.2, 4.8, 0.859, 0.543}},
+                                         {{2.9, 3.2, 0.405, 0.158}, {2.7, 4.9, 0.655, 0.282}, {3.1, 6.2, 0.840, 0.486}},
+                                         {{2.8, 2.6, 0.426, 0.161}, {3.1, 3.6, 0.902, 0.158}, {2.6, 3.9, 0.910, 0.470}},
+                                         {{4.1, 2.4, 0.519, 0.100}, {4.3, 3.5, 1.075, 0.140}, {3.4, 5.2, 0.982, 0.676}}};
 struct FewCost {
     double launch, round, copy, memory;            // copy: bytes per ns and CU; memory: bytes per us / 1e6
 };
-constexpr FewCost kRaggedFew[2] = {{3.6, 2.3, 75.7, 5.8}, {4.4, 2.4, 77.2, 6.2}};
+constexpr FewCost kRaggedFew[2] = {{3.1, 2.3, 74.2, 5.6}, {4.5, 2.4, 75.8, 6.2}};
 
 double expected_tiles(double M, double live, int rows) {
     const double t = M / rows + 0.5 * live;
@@ -93,8 +93,11 @@ double expected_tiles(double M, double live, int rows) {
 
 double ragged_time(RaggedOp op, int c, double tiles, double steps) {
     const ClassCost &k = kRaggedCost[op][c];
-    const double full = tiles < 256 ? tiles / 256.0 : 1.0;
-    return k.launch + (double)cdiv((int64_t)tiles, 256) * (k.wave + steps * (k.step + k.load * full));
+    const int64_t n = (int64_t)tiles, left = n % 256;
+    double rounds = (double)(n / 256) + (left == 0 ? 0.0 : (left <= 128 ? 0.7 : 1.0));
+    if (rounds < 0.7) rounds = 0.7;
+    const double busy = n >= 256 ? 1.0 : (double)(left <= 128 ? 2 * left : left) / 256.0;
+    return k.launch + rounds * (k.wave + steps * (k.step + k.load * busy));
 }
 
 // M rows [K] of G experts times weights [N][K] (op R_TOKEN_GRAD: N and K are

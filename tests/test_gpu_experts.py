@@ -106,8 +106,8 @@ def builds(op):
     """{build: the cheapest of the candidate sizes that takes it}."""
     import fp8_gemm_amd as f
     best = {}
-    long = (1152, 1168) if op == 1 else (576, 584)
-    for m in (3, 17, 40, 100, 130, 200, 300, 500, 700, 1000, 1500, 2000, 3000, 5000):
+    long = (1152, 1168) if op == 1 else ((576, 1024, 2832) if op == 3 else (576, 584))
+    for m in (3, 17, 40, 100, 130, 200, 300, 500, 700, 1000, 1500, 2000, 3000, 5000, 9000):
         for x in (8, 24, 40, 64, 136, 264, 520, 1032, 2056, 4104, 8200):
             for red in long:
                 for g in (1, 2, 4, 7, 16, 40, 70):
