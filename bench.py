@@ -65,7 +65,8 @@ def log(msg):
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     for f in ("kernels.hpp", "device_common.hpp", "fp8_gemm.hip", "fused.hpp", "fused_bf16.hpp", "fused_host.hpp",
-              "fused_fp8.hip", "fused_bf16.hip"):
+              "fused_fp8.hip", "fused_bf16.hip", "ragged.hpp", "tile_halves.hpp", "experts.hpp", "quantize.hpp",
+              "experts_host.hpp", "experts_bf16.hip", "experts_int8.hip"):
         with open(os.path.join(ROOT, "fp8_gemm_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
@@ -569,13 +570,28 @@ COUNTER_TARGETS = {
     "gated_bf16_weight_grad": ("bf16_tile_kernel_gated_weight_grad_4096x14336x4096",
                                "bf16_tile_kernel<256, 256, 2, true, true, false, 0>",
                                "gated BF16 backward pass M=4096 N=14336 K=4096, silu (seed 25): weight gradients"),
+    "experts_bf16": ("ragged_tile_kernel_experts_8x14336x4096", "ragged_tile_kernel<256, 256, 2, false, false, false, false, 1, 0>",
+                     "BF16 products of 8 experts N=14336 K=4096 over 8192 uneven rows (seed 26)"),
+    "experts_token_grad": ("ragged_tile_kernel_token_grad_8x14336x4096",
+                           "ragged_tile_kernel<256, 256, 2, false, false, true, false, 2, 0>",
+                           "their backward pass (seed 26): token gradient"),
+    "experts_weight_grad": ("ragged_tile_kernel_weight_grad_8x14336x4096",
+                            "ragged_tile_kernel<256, 256, 2, false, true, true, false, 3, 0>",
+                            "their backward pass (seed 26): weight gradients"),
+    "int8_prompt": ("int8_tile_kernel_4096x14336x4096", "int8_tile_kernel<256, 256, 2, false, 4>",
+                    "product in 8-bit integers M=4096 N=14336 K=4096, scales per row and channel (seed 27)"),
+    "experts_int8_decode": ("ragged_decode_kernel_experts_64x2048x7168", "ragged_decode_kernel<4, 1, true, 2>",
+                            "products in 8-bit integers of 64 experts N=2048 K=7168 over 512 rows, 8 each (seed 28)"),
+    "quantize": ("quantize_rows_kernel_8192x14336", "quantize_rows_kernel<256, 8>", "quantisation of 8192 rows of 14336 (seed 29)"),
 }
 # Dense matrix-core FLOPs per SIMD per cycle of each target's instruction
 # (FP8 by default; BF16 runs at half that rate).
-FUSED_BF16_TARGETS = ("fused_bf16_2048", "fused_bf16_4096", "gated_bf16_token_grad", "gated_bf16_weight_grad")
+FUSED_BF16_TARGETS = ("fused_bf16_2048", "fused_bf16_4096", "gated_bf16_token_grad", "gated_bf16_weight_grad",
+                      "experts_bf16", "experts_token_grad", "experts_weight_grad")
 MFMA_FLOPS_PER_CYCLE = {"dense_4096_bf16": 1024.0, **{t: 1024.0 for t in FUSED_BF16_TARGETS}}
 MFMA_COUNT_NOTE = {"dense_4096_bf16": "each 32x32x16 BF16 instruction as 32 cycles, 1024 FLOPs per cycle",
-                   **{t: "each 16x16x32 BF16 instruction as 16 cycles, 1024 FLOPs per cycle" for t in FUSED_BF16_TARGETS}}
+                   **{t: "each 16x16x32 BF16 instruction as 16 cycles, 1024 FLOPs per cycle" for t in FUSED_BF16_TARGETS},
+                   **{t: "each 16x16x64 integer instruction as 16 cycles" for t in ("int8_prompt", "experts_int8_decode")}}
 COPY_PATTERN = "neg_kernel"
 PROFILE_LAUNCHES = 6
 
@@ -706,6 +722,7 @@ def profile_run(targets=None):
                                                              + wc.sa.nbytes + wc.sb.nbytes)}
         del a, b, sa, sb, gi, out, wc
     profile_fused(torch, f, on, work)
+    profile_experts(torch, f, on, work)
     print(json.dumps({"profile_run": True, "work": work}), flush=True)
 
 
@@ -751,6 +768,53 @@ def profile_fused(torch, f, on, work):
         work["gated_bf16_grad"] = {"flops": 0.0, "bytes": float(M * N * (2 + 8 + 4))}
         work["gated_bf16_token_grad"] = {"flops": 4.0 * M * N * K, "bytes": float(2 * (2 * M * N + 2 * N * K + M * K))}
         work["gated_bf16_weight_grad"] = {"flops": 4.0 * M * N * K, "bytes": float(2 * (2 * M * N + M * K + 2 * N * K))}
+
+
+def profile_experts(torch, f, on, work):
+    """The experts' and integer counter targets of profile_run, seeded on the device."""
+    def normal(seed, *shape, std=1.0, dtype=torch.bfloat16):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        return torch.randn(*shape, generator=g, device="cuda").mul_(std).to(dtype)
+
+    def codes(seed, *shape):
+        return normal(seed, *shape, std=30.0, dtype=torch.float32).clamp_(-127, 127).to(torch.int8)
+
+    def launch(name, call):
+        log(f"profile: {COUNTER_TARGETS[name][2]}")
+        for _ in range(PROFILE_LAUNCHES):
+            call()
+        torch.cuda.synchronize()
+
+    if on("experts_bf16") or on("experts_token_grad") or on("experts_weight_grad"):
+        rows, N, K = (700, 1390, 1010, 830, 1220, 960, 1300, 782), 14336, 4096
+        M, G = sum(rows), len(rows)
+        offsets = torch.tensor([0, *rows]).cumsum(0).to(torch.int32).cuda()
+        a, b, grad = normal(26, M, K), normal(126, G, N, K, std=0.02), normal(226, M, N)
+        d = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        launch("experts_bf16", lambda: f.grouped_gemm_ragged_bf16(a, b, offsets, out=d))
+        launch("experts_token_grad", lambda: f.grouped_gemm_ragged_bf16_backward(grad, a, b, offsets))
+        for name in ("experts_bf16", "experts_token_grad", "experts_weight_grad"):
+            work[name] = {"flops": 2.0 * M * N * K, "bytes": float(2 * (M * K + G * N * K + M * N))}
+        del a, b, grad, d
+    if on("int8_prompt"):
+        M, N, K = 4096, 14336, 4096
+        a, b = codes(27, M, K), codes(127, N, K)
+        s = torch.full((M,), 0.01, device="cuda"), torch.full((N,), 0.02, device="cuda")
+        launch("int8_prompt", lambda: f.gemm_nt_int8(a, b, *s))
+        work["int8_prompt"] = {"flops": 2.0 * M * N * K, "bytes": float(M * K + N * K + 2 * M * N + 4 * (M + N))}
+    if on("experts_int8_decode"):
+        G, N, K, M = 64, 2048, 7168, 512
+        offsets = torch.arange(0, M + 1, M // G, dtype=torch.int32, device="cuda")
+        a, b = codes(28, M, K), codes(128, G, N, K)
+        s = torch.full((M,), 0.01, device="cuda"), torch.full((G, N), 0.02, device="cuda")
+        launch("experts_int8_decode", lambda: f.grouped_gemm_ragged_int8(a, b, offsets, *s))
+        work["experts_int8_decode"] = {"flops": 2.0 * M * N * K, "bytes": float(M * K + G * N * K + 2 * M * N + 4 * (M + G * N))}
+    if on("quantize"):
+        M, K = 8192, 14336
+        x = normal(29, M, K)
+        launch("quantize", lambda: f.quantize_rows_int8(x))
+        work["quantize"] = {"flops": 0.0, "bytes": float(3 * M * K + 4 * M)}
 
 
 def _csv_files(directory, suffix):

@@ -15,15 +15,16 @@ namespace fp8g {
 // Tiles of one expert's rows (tile_halves_body with the placements of
 // ragged.hpp).
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int STAGES, int FMT, bool TA, bool TB, bool TAIL, int PLACE, int EPI>
-__global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedParams<EPI, FMT == FMT_I8, PLACE> p) {
-    tile_halves_body<BM, BN, STAGES, FMT, TA, TB, TAIL, PLACE>(p);
+template <int BM, int BN, int STAGES, bool INT, bool TA, bool TB, bool TAIL, int PLACE, int EPI>
+__global__ __launch_bounds__(256, 1) void ragged_tile_kernel(RaggedParams<EPI, INT, PLACE> p) {
+    tile_halves_body<BM, BN, STAGES, INT ? FMT_I8 : FMT_BF16, TA, TB, TAIL, PLACE>(p);
 }
 
 // Few rows per expert: 16 CB rows of one expert times 16 RB of its weight rows
 // per workgroup, the waves splitting K (decode_body).
-template <int RB, int CB, int FMT, int D>
-__global__ __launch_bounds__(256, 2) void ragged_decode_kernel(RaggedParams<EPI_ACT, FMT == FMT_I8, PLACE_GROUPS> p) {
+template <int RB, int CB, bool INT, int D>
+__global__ __launch_bounds__(256, 2) void ragged_decode_kernel(RaggedParams<EPI_ACT, INT, PLACE_GROUPS> p) {
+    constexpr int FMT = INT ? FMT_I8 : FMT_BF16;
     decode_body<4, RB, CB, FMT, FMT, D, SCALE_CHANNEL>(p);
 }
 

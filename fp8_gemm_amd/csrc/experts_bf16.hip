@@ -4,7 +4,6 @@
 namespace {
 
 using fp8g::EPI_STORE;
-using fp8g::FMT_BF16;
 
 template <int BM, int BN, int STAGES>
 int launch_sums_shape(const FusedArgs &a, const int32_t *offsets, int rows, hipStream_t s) {
@@ -19,7 +18,7 @@ int launch_sums_shape(const FusedArgs &a, const int32_t *offsets, int rows, hipS
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     if (const int st = check_grid(tiles * p.G)) return st;
     const dim3 grid((unsigned)persistent_grid(tiles * p.G)), block(256);
-    hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, FMT_BF16, true, true, false, PLACE_SUMS, EPI_STORE>), grid,
+    hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, false, true, true, false, PLACE_SUMS, EPI_STORE>), grid,
                        block, 0, s, p);
     return launch_status("ragged weight gradient kernel");
 }
@@ -82,9 +81,9 @@ int bf16_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t 
         return st;
     FusedArgs p = ragged_args(A, lda, B, ldb, b_stride, D, ldd, M, G, N, K, 2);
     const Choice c = pick_ragged(R_BF16, M, G, N, K);
-    if (c.c != C_FEW) return launch_rows<FMT_BF16, false, PLACE_GROUPS, EPI_STORE>(c.c, p, offsets, static_cast<hipStream_t>(stream));
+    if (c.c != C_FEW) return launch_rows<false, false, PLACE_GROUPS, EPI_STORE>(c.c, p, offsets, static_cast<hipStream_t>(stream));
     p.K *= 2;
-    return launch_ragged_few_shape<FMT_BF16>(p, c.few, offsets, static_cast<hipStream_t>(stream));
+    return launch_ragged_few_shape<false>(p, c.few, offsets, static_cast<hipStream_t>(stream));
 }
 
 int bf16_grouped_gemm_ragged_backward(const void *dD, int64_t ldg, const void *A, int64_t lda, const void *B,
@@ -115,7 +114,7 @@ int bf16_grouped_gemm_ragged_backward(const void *dD, int64_t ldg, const void *A
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (want_a) {
         const FusedArgs p = ragged_args(dD, ldg, B, ldb, b_stride, dA, ldda, M, G, K, N, 2);
-        if ((st = launch_rows<FMT_BF16, true, PLACE_REST, EPI_STORE>(pick_ragged(R_TOKEN_GRAD, M, G, K, N).c, p, offsets, s))) return st;
+        if ((st = launch_rows<false, true, PLACE_REST, EPI_STORE>(pick_ragged(R_TOKEN_GRAD, M, G, K, N).c, p, offsets, s))) return st;
     }
     if (want_b) {
         FusedArgs p = ragged_args(dD, ldg, A, lda, 0, dB, lddb, N, G, K, M, 2);

@@ -176,49 +176,49 @@ int check_grid(int64_t workgroups) {
 // Persistent workgroups: one per CU (few tiles are cut in two).
 int64_t persistent_grid(int64_t tiles) { return 2 * tiles < 256 ? 2 * tiles : 256; }
 
-template <int BM, int BN, int STAGES, int FMT, bool TB, int PLACE, int EPI>
+template <int BM, int BN, int STAGES, bool INT, bool TB, int PLACE, int EPI>
 int launch_rows_shape(const FusedArgs &a, const int32_t *offsets, hipStream_t s) {
-    auto p = with_offsets<EPI, FMT == fp8g::FMT_I8, PLACE>(a, offsets);
+    auto p = with_offsets<EPI, INT, PLACE>(a, offsets);
     p.tiles_n = (int)cdiv(p.N, BN);
     const int64_t wgs = tiles_bound(p.M, p.G + (PLACE == PLACE_REST ? 2 : 0), BM) * p.tiles_n;
     if (const int st = check_grid(wgs)) return st;
     const dim3 grid((unsigned)persistent_grid(wgs)), block(256);
-    if (p.K % (FMT == fp8g::FMT_I8 ? 128 : 64))
-        hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, FMT, false, TB, true, PLACE, EPI>), grid, block, 0, s, p);
+    if (p.K % (INT ? 128 : 64))
+        hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, INT, false, TB, true, PLACE, EPI>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, FMT, false, TB, false, PLACE, EPI>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, INT, false, TB, false, PLACE, EPI>), grid, block, 0, s, p);
     return launch_status("ragged tiled kernel");
 }
 
-template <int FMT, bool TB, int PLACE, int EPI>
+template <bool INT, bool TB, int PLACE, int EPI>
 int launch_rows(ShapeClass c, const FusedArgs &a, const int32_t *offsets, hipStream_t s) {
-    if (c == C_128x128) return launch_rows_shape<128, 128, 4, FMT, TB, PLACE, EPI>(a, offsets, s);
-    if (c == C_128x256) return launch_rows_shape<128, 256, 3, FMT, TB, PLACE, EPI>(a, offsets, s);
-    return launch_rows_shape<256, 256, 2, FMT, TB, PLACE, EPI>(a, offsets, s);
+    if (c == C_128x128) return launch_rows_shape<128, 128, 4, INT, TB, PLACE, EPI>(a, offsets, s);
+    if (c == C_128x256) return launch_rows_shape<128, 256, 3, INT, TB, PLACE, EPI>(a, offsets, s);
+    return launch_rows_shape<256, 256, 2, INT, TB, PLACE, EPI>(a, offsets, s);
 }
 
 // Few rows per expert (K and the strides in bytes).
-template <int RB, int CB, int FMT>
+template <int RB, int CB, bool INT>
 int launch_ragged_few(const FusedArgs &a, const int32_t *offsets, hipStream_t s) {
-    const auto p = with_offsets<fp8g::EPI_ACT, FMT == fp8g::FMT_I8, PLACE_GROUPS>(a, offsets);
+    const auto p = with_offsets<fp8g::EPI_ACT, INT, PLACE_GROUPS>(a, offsets);
     const dim3 grid((unsigned)cdiv(p.N, 16 * RB), (unsigned)tiles_bound(p.M, p.G, 16 * CB)), block(256);
     if (const int st = check_grid((int64_t)grid.x * grid.y)) return st;
-    hipLaunchKernelGGL((fp8g::ragged_decode_kernel<RB, CB, FMT, few_slots(RB, CB)>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((fp8g::ragged_decode_kernel<RB, CB, INT, few_slots(RB, CB)>), grid, block, 0, s, p);
     return launch_status("ragged few-token kernel");
 }
 
-template <int RB, int FMT>
+template <int RB, bool INT>
 int launch_ragged_few_rb(const FusedArgs &a, int cb, const int32_t *offsets, hipStream_t s) {
-    if (cb == 1) return launch_ragged_few<RB, 1, FMT>(a, offsets, s);
-    if (cb == 2) return launch_ragged_few<RB, 2, FMT>(a, offsets, s);
-    return launch_ragged_few<RB, 4, FMT>(a, offsets, s);
+    if (cb == 1) return launch_ragged_few<RB, 1, INT>(a, offsets, s);
+    if (cb == 2) return launch_ragged_few<RB, 2, INT>(a, offsets, s);
+    return launch_ragged_few<RB, 4, INT>(a, offsets, s);
 }
 
-template <int FMT>
+template <bool INT>
 int launch_ragged_few_shape(const FusedArgs &a, const FewShape &f, const int32_t *offsets, hipStream_t s) {
-    if (f.rb == 1) return launch_ragged_few_rb<1, FMT>(a, f.cb, offsets, s);
-    if (f.rb == 2) return launch_ragged_few_rb<2, FMT>(a, f.cb, offsets, s);
-    return launch_ragged_few_rb<4, FMT>(a, f.cb, offsets, s);
+    if (f.rb == 1) return launch_ragged_few_rb<1, INT>(a, f.cb, offsets, s);
+    if (f.rb == 2) return launch_ragged_few_rb<2, INT>(a, f.cb, offsets, s);
+    return launch_ragged_few_rb<4, INT>(a, f.cb, offsets, s);
 }
 
 // A product of rows [M][lda] with experts' weights; strides in bytes.

@@ -83,8 +83,8 @@ int int8_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t 
     p.act = FP8G_ACT_NONE;
     const Choice c = pick_ragged(R_INT8, M, G, N, K);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (c.c == C_FEW) return launch_ragged_few_shape<FMT_I8>(p, c.few, offsets, s);
-    return launch_rows<FMT_I8, false, PLACE_GROUPS, EPI_SCALED>(c.c, p, offsets, s);
+    if (c.c == C_FEW) return launch_ragged_few_shape<true>(p, c.few, offsets, s);
+    return launch_rows<true, false, PLACE_GROUPS, EPI_SCALED>(c.c, p, offsets, s);
 }
 
 int int8_gemm_nt_fused(const void *A, int64_t lda, const void *B, int64_t ldb, const float *scale_a, int scale_a_n,

@@ -8,7 +8,7 @@ kernels' rules):
 * the persistent kernels read their sums only after the wait that the pins hide
   from the compiler: the last matrix instruction before an accumulator is read
   is at least 20 wait states back;
-* no build copies its sums between the register files in its main loop.
+* no build copies sums between the register files in its main loop.
 """
 import os
 import re
@@ -86,8 +86,7 @@ def test_main_loops_keep_their_sums(asm, unit):  # noqa: F811
             mfma = sum(s.startswith("v_mfma") for s in body)
             if mfma >= 8:
                 loops += 1
-                moves = [s for s in body if s.startswith("v_accvgpr")]
-                # (a loop's last block may go on into the clearing of the next tile's sums)
+                # (the loop's last block may go on into the clearing of the next tile's sums)
                 back = next((i for i, s in enumerate(body) if s.startswith("s_cbranch") and s.split()[1] == label), len(body))
-                assert not [s for s in body[:back] if s.startswith("v_accvgpr")] or not moves, f"{name} {label}: {moves[0]}"
+                assert not [s for s in body[:back] if s.startswith("v_accvgpr")], f"{name} {label}"
     assert loops >= 15
