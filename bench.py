@@ -582,7 +582,7 @@ COUNTER_TARGETS = {
                     "product in 8-bit integers M=4096 N=14336 K=4096, scales per row and channel (seed 27)"),
     "experts_int8_decode": ("ragged_decode_kernel_experts_64x2048x7168", "ragged_decode_kernel<4, 1, true, 2>",
                             "products in 8-bit integers of 64 experts N=2048 K=7168 over 512 rows, 8 each (seed 28)"),
-    "quantize": ("quantize_rows_kernel_8192x14336", "quantize_rows_kernel<256, 8>", "quantisation of 8192 rows of 14336 (seed 29)"),
+    "quantize": ("quantize_rows_kernel_8192x14336", "quantize_rows_kernel<1024, 2>", "quantisation of 8192 rows of 14336 (seed 29)"),
 }
 # Dense matrix-core FLOPs per SIMD per cycle of each target's instruction
 # (FP8 by default; BF16 runs at half that rate).

@@ -180,8 +180,9 @@ template <int BM, int BN, int STAGES, bool INT, bool TB, int PLACE, int EPI>
 int launch_rows_shape(const FusedArgs &a, const int32_t *offsets, hipStream_t s) {
     auto p = with_offsets<EPI, INT, PLACE>(a, offsets);
     p.tiles_n = (int)cdiv(p.N, BN);
-    const int64_t wgs = tiles_bound(p.M, p.G + (PLACE == PLACE_REST ? 2 : 0), BM) * p.tiles_n;
+    const int64_t bound = tiles_bound(p.M, p.G + (PLACE == PLACE_REST ? 2 : 0), BM), wgs = bound * p.tiles_n;
     if (const int st = check_grid(wgs)) return st;
+    p.tiles_m = (int)bound;
     const dim3 grid((unsigned)persistent_grid(wgs)), block(256);
     if (p.K % (INT ? 128 : 64))
         hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, INT, false, TB, true, PLACE, EPI>), grid, block, 0, s, p);

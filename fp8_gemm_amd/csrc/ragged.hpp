@@ -55,9 +55,11 @@ struct RaggedTiles {
         upto = wave_scan((hi - lo + BM - 1) / BM, lane);
         return __builtin_amdgcn_readlane(upto, 63);
     }
-    __device__ __forceinline__ int count() {
+    // The number of tiles, of which `most` (below 2^24) suffice for offsets that
+    // do not decrease.
+    __device__ __forceinline__ int count(int most) {
         int n = 0;
-        for (int first = 0; first < segments(); first += 64) n += read(first);
+        for (int first = 0; first < segments(); first += 64) n = min(max(n + read(first), 0), most);
         return n;
     }
     // Tile t: expert (-1: a tile of zeros), first row, rows; false if there is
@@ -75,6 +77,8 @@ struct RaggedTiles {
                 const int begin = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
                 const int tiles = (end - begin + BM - 1) / BM;
                 const int nth = t - (__builtin_amdgcn_readlane(upto, l) - tiles);
+                // (offsets that decrease can overflow the sums of tiles)
+                if ((unsigned)nth >= (unsigned)tiles) return false;
                 s.g = REST && (g < 0 || g >= G) ? -1 : g;
                 s.m0 = begin + nth * BM;
                 s.rows = min(BM, end - s.m0);

@@ -135,7 +135,7 @@ __device__ __forceinline__ void tile_halves_body(P p) {
     if constexpr (PERSIST) {
         if constexpr (PLACE == PLACE_GROUPS || PLACE == PLACE_REST) {
             tiles = Tiles{p.offsets, p.G, p.M, lane, 0, 0, 0};
-            row_tiles = tiles.count();
+            row_tiles = tiles.count(p.tiles_m);
         } else {
             row_tiles = PLACE == PLACE_SUMS ? p.G * p.tiles_m : p.tiles_m;
         }

@@ -261,6 +261,14 @@ def test_bad_offsets_stay_inside(f, M, N, K):
         ga, gb = f.grouped_gemm_ragged_bf16_backward(out.clone(), a, b, o)
         torch.cuda.synchronize()
         assert (buf[:32] == 7).all() and (buf[32 + M:] == 7).all() and ga.shape == a.shape and gb.shape == b.shape
+    # far more tiles than any offsets that do not decrease can make, in one batch of 64 experts and in several
+    for G in (60, 200):
+        many = torch.zeros(G, N, K, dtype=BF, device=DEV)
+        o = torch.tensor([0, M] * (G // 2) + [0], dtype=torch.int32, device=DEV)
+        f.grouped_gemm_ragged_bf16(a, many, o, out=out)
+        ga, gb = f.grouped_gemm_ragged_bf16_backward(out.clone(), a, many, o)
+        torch.cuda.synchronize()
+        assert (buf[:32] == 7).all() and (buf[32 + M:] == 7).all()
     # values past either end count as that end
     o = torch.tensor([-5, 10, 20, 40, 2147483647], dtype=torch.int32, device=DEV)
     E.check_rows(f.grouped_gemm_ragged_bf16(a, b, o), a, b, [10, 10, 20, M - 40], 0, columns(N), "clamped")
