@@ -1615,6 +1615,10 @@ __global__ __launch_bounds__(256, 1) void swap_kernel(GemmParams p) {
 // each weight matrix, in turn: block 2 q holds rows 16 q .. + 15 of p.B, block
 // 2 q + 1 the same rows of p.B2.  BF16 operands arrive with K, lda and ldb in
 // bytes: a 128-byte K step is 64 elements, two instructions per block pair.
+// 8-bit integers: 128 elements, two instructions as well, and 32-bit sums.
+//
+// Ragged groups (P::kPlace): grid y counts tiles of 16 CB rows of one expert
+// (ragged.hpp), whose rows and weights are all that the workgroup sees.
 // ---------------------------------------------------------------------------
 template <int WAVES, int RB, int CB, int FA, int FB, int D, int SCL, class P>
 __device__ __forceinline__ void decode_body(P p) {

@@ -8,12 +8,11 @@ namespace fp8g {
 // ---------------------------------------------------------------------------
 // Quantisation of rows.  T threads hold one row in registers, 8 values per
 // thread and chunk, up to R chunks: one pass over memory (2 bytes read, 1
-// written per value), which bounds it: 8192 x 14336 values 60.9 us, 5.8 TB/s; a
-// few rows take launch and the latency of one load (16 x 14336: 3.2 us).  The
-// maximum is that of the BF16 magnitudes as integers,
-// which also orders infinities and NaN behind every finite value: a row that
-// holds one gets the scale NaN (and codes 0), so that every product of the
-// row is NaN.
+// written per value), which bounds it: 8192 x 14336 values 61.4 us, 5.7 TB/s; a
+// few rows take the launch and the latency of one load (16 x 14336: 3.6 us).
+// The maximum is that of the BF16 magnitudes as integers, which also orders
+// infinities and NaN behind every finite value: a row that holds one gets the
+// scale NaN (and codes 0), so that every product of the row is NaN.
 //
 // Each code is round(127 x / a), a the row's largest magnitude, rounded to
 // even at halves, exactly: t = 127 x has 15 significant bits and is exact in

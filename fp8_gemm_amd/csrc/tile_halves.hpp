@@ -61,10 +61,10 @@ namespace fp8g {
 // the offsets behind the epilogue.  Tiles of at most BM / 2 rows (an expert's
 // last rows, the cut tiles of the last round) run a step of half the matrix
 // instructions, which takes about 0.7 of a whole one's time: 4096 x 14336 x 4096
-// in 8-bit integers, 3.5 rounds, 194 -> 174 us.  They stay in the order of
-// the rows: moved behind all whole tiles, for a balanced end, each expert's
-// weights came from memory twice, 8 experts of 14336 x 4096 over 8192 rows 795
-// against 757 us.
+// in 8-bit integers, 3.5 rounds, 196 -> 189 us; 2048 x 4096 x 14336, half a
+// round, 121 -> 95 us.  They stay in the order of the rows: moved behind all
+// whole tiles, for a balanced end, each expert's weights came from memory twice,
+// 8 experts of 14336 x 4096 over 8192 rows 795 against 757 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int strided_key(int k) { return 2 * (k & 3) + ((k >> 3) & 1); }
 

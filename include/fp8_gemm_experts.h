@@ -45,8 +45,8 @@ extern "C" {
  * Ragged grouped product, BF16:
  *   D[r][n] = bf16_rne( sum_k A[r][k] B[g][n][k] )   for the rows r of expert g
  *   A [M][lda], D [M][ldd] BF16, 16-byte aligned; ldd at most (2^23 - 16) / 2,
- *   as every output's stride here.  Rows of no expert are
- *   neither read from A nor written to D.  K = 0 writes zeros.
+ *   as every output's stride here.  Rows of no expert are neither read from A
+ *   nor written to D.  K = 0 writes zeros.
  * Few rows per expert take the few-token kernel (16, 32 or 64 weight rows per
  * workgroup, tiles of 16, 32 or 64 rows of one expert), more the LDS-tiled one
  * (128 x 128, 128 x 256 or 256 x 256); the choice goes by an estimate of the
