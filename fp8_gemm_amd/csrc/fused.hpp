@@ -27,7 +27,6 @@ constexpr int EPI_SCALED = 4;
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
 
 struct FusedArgs : GemmParams {
-    static constexpr bool kIntSums = false;        // the tiles' sums are 32-bit integers
     // Gated: the second weight matrix and its channel scales (p.B / ch_sb: the
     // first).  K-strided B of the backward pass: the rows of K steps from
     // ksplit on.
@@ -50,20 +49,20 @@ struct FusedArgs : GemmParams {
     int ksplit, krows;
 };
 
-// SCALED: the sums take scales (FP8); BF16 sums do not.
-template <int E, bool SCALED>
+// SCALED: the sums take scales (FP8, 8-bit integers); BF16 sums do not.  INT:
+// they are 32-bit integers.
+template <int E, bool SCALED, bool INT = false>
 struct FusedParams : FusedArgs {
     static constexpr int kEpilogue = E;
     static constexpr bool kScaled = SCALED;
+    static constexpr bool kIntSums = INT;
 };
 
 // 8-bit integers (experts.hpp): the sums are staged as they are and become FP32
 // (rounded to nearest even) where the epilogue reads them.  Converted before,
 // they took registers that the 256 x 256 tile does not have (5 spilled).
 template <int E>
-struct Int8Params : FusedParams<E, true> {
-    static constexpr bool kIntSums = true;
-};
+struct Int8Params : FusedParams<E, true, true> {};
 
 // Over ragged groups of rows (ragged.hpp): expert g's weights begin b_gstride
 // bytes after those of expert g - 1, its channel scales N floats, its weight
@@ -71,9 +70,8 @@ struct Int8Params : FusedParams<E, true> {
 // and N are the gradient's); stream: its stores bypass the caches.  Scales
 // come with 8-bit integers only.
 template <int E, bool SCALED, int PLACE>
-struct RaggedParams : FusedParams<E, SCALED> {
+struct RaggedParams : FusedParams<E, SCALED, SCALED> {
     static constexpr int kPlace = PLACE;
-    static constexpr bool kIntSums = SCALED;
     const int32_t *offsets;
     int rows, stream;
 };
@@ -194,6 +192,26 @@ __device__ __forceinline__ ColumnTerms<NV> column_terms(const P &p, int n, int n
     return t;
 }
 
+// The scale of a row of integer sums in two factors, for z first (sb rest).  A
+// sum of up to 2^31 times a scale above 2^96 could leave FP32 although the
+// output, with a small channel scale, does not (rows quantised from values above
+// 2^103): such a row leaves 2^32 of its scale to the channel's.  At the other end
+// nothing is lost: whole multiples of a scale below the normal numbers are exact
+// there.  Both factors are powers of two away from the scale, so that no output
+// within FP32 depends on the split.  (Where both scales are above 2^96, every sum
+// but 0 leaves FP32, and 0 becomes NaN.)  It costs one product per output: 0.4 to
+// 0.8% of prompts (4096 x 14336 x 4096 191.6 against 190.5 us), 1.6% where K is
+// short (8192 x 8192 x 512 57.9 against 56.9), 0.16 us of few tokens.  A branch
+// around it, per 4 outputs or with the whole epilogue twice, took more: scalar
+// instructions in every pass, or 8 to 41 spilled registers.
+struct RowFactors {
+    float first, rest;
+};
+__device__ __forceinline__ RowFactors row_factors(float sa) {
+    const bool large = __builtin_fabsf(sa) > 0x1p+96f;
+    return {large ? sa * 0x1p-32f : sa, large ? 0x1p+32f : 1.0f};
+}
+
 // The epilogue of NV consecutive outputs of row m from column n on (z: the
 // sums; gated: z of the first matrix, z2 of the second; sa: the row's scale;
 // r: the residual): scales and bias, the pre-activations kept for the backward
@@ -203,9 +221,10 @@ template <int ACT, int NV, class P>
 __device__ __forceinline__ void fused_outputs(const P &p, int m, int n, int nv, const ColumnTerms<NV> &t, float sa,
                                               const float (&r)[NV], float (&z)[NV], float (&z2)[NV], float (&out)[NV]) {
     constexpr bool GATED = P::kEpilogue == EPI_GATED;
+    const RowFactors f = P::kIntSums ? row_factors(sa) : RowFactors{sa, 1.0f};
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-        if (P::kScaled) z[e] = z[e] * sa * t.s[e];
+        if (P::kScaled) z[e] = z[e] * f.first * (P::kIntSums ? t.s[e] * f.rest : t.s[e]);
         if (P::kScaled && GATED) z2[e] = z2[e] * sa * t.s2[e];
         if (!GATED) z[e] += t.b[e];
     }
@@ -429,7 +448,7 @@ __global__ __launch_bounds__(256, 1) void fused_tile16_kernel(FusedParams<EPI, t
 // plain product there).  (Builds for one workgroup per CU, as the dense form
 // has for grids of up to 256, measured within 1% of these for two.)
 template <int WAVES, int RB, int CB, int FA, int FB, int D, int EPI>
-__global__ __launch_bounds__(64 * WAVES, 2) void fused_decode_kernel(FusedParams<EPI, FA != FMT_BF16> p) {
+__global__ __launch_bounds__(64 * WAVES, 2) void fused_decode_kernel(FusedParams<EPI, FA != FMT_BF16, FA == FMT_I8> p) {
     decode_body<WAVES, RB, CB, FA, FB, D, SCALE_CHANNEL>(p);
 }
 

@@ -16,9 +16,9 @@ using namespace fp8g_host;
 using fp8g::FusedArgs;
 using fp8g::FusedParams;
 
-template <int E, bool SCALED>
-FusedParams<E, SCALED> with_epilogue(const FusedArgs &a) {
-    FusedParams<E, SCALED> p = {};
+template <int E, bool SCALED, bool INT = false>
+FusedParams<E, SCALED, INT> with_epilogue(const FusedArgs &a) {
+    FusedParams<E, SCALED, INT> p = {};
     static_cast<FusedArgs &>(p) = a;
     return p;
 }
@@ -260,7 +260,7 @@ BackwardShape backward_shape(int64_t M, int64_t N, int64_t K, int ny) {
 // ---------------------------------------------------------------------------
 template <int RB, int CB, int FA, int FB, int EPI>
 int launch_few(const FusedArgs &a, int64_t workgroups, hipStream_t s) {
-    const auto p = with_epilogue<EPI, FA != fp8g::FMT_BF16>(a);
+    const auto p = with_epilogue<EPI, FA != fp8g::FMT_BF16, FA == fp8g::FMT_I8>(a);
     const unsigned tiles = (unsigned)cdiv(p.M, 64);
     const dim3 grid((unsigned)(workgroups / tiles), tiles), block(64 * kFewWaves);
     hipLaunchKernelGGL((fp8g::fused_decode_kernel<kFewWaves, RB, CB, FA, FB, few_slots(RB, CB), EPI>), grid, block, 0, s, p);

@@ -435,11 +435,12 @@ __device__ __forceinline__ void tile_halves_body(P p) {
             const float *const tf = reinterpret_cast<const float *>(terms);
             v4u held[2];
             uint32_t at[2];
+            RowFactors sa = {1.0f, 1.0f};          // of the 16 rows at hand
             static_for<PASSES + 1>([&](auto pc) {
                 constexpr int pass = pc.value, j = pass / PASS_N, h = pass % PASS_N;
                 v4u v[2];
                 if constexpr (pass < PASSES) {
-                    const float sa = EPI == EPI_SCALED ? tf[row_block(j) * 16 + r16] : 1.0f;
+                    if constexpr (EPI == EPI_SCALED && h == 0) sa = row_factors(tf[row_block(j) * 16 + r16]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         v4f z = sums_f32(acc[h * 4 + i][j]);
@@ -447,7 +448,7 @@ __device__ __forceinline__ void tile_halves_body(P p) {
                             const int c = wn * TN + (h * 4 + i) * 16 + kg * 4;
                             const v4f sb = *reinterpret_cast<const v4f *>(tf + 256 + c), b = *reinterpret_cast<const v4f *>(tf + 512 + c);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) z[e] = z[e] * sa * sb[e] + b[e];
+                            for (int e = 0; e < 4; ++e) z[e] = z[e] * sa.first * (sb[e] * sa.rest) + b[e];
                         }
                         *reinterpret_cast<v2u *>(st + put[i]) = pack_bf16x4(z[0], z[1], z[2], z[3]);
                     }
