@@ -41,6 +41,10 @@ struct RaggedTiles {
     int G, M, lane;
     int lo, hi, upto;          // of the lane's expert in the batch read last: its rows, the tiles up to and with it
 
+    // Tiles of a segment's rows (the sum in 32 bits without a sign: up to 2^31 - 1
+    // rows, and a tile's more).
+    __device__ __forceinline__ static int tiles_of(int rows) { return (int)(((unsigned)rows + (BM - 1)) / BM); }
+
     // Segment j: expert j, or with REST expert j - 1 between the rows before
     // the first expert (j = 0) and those behind the last (j = G + 1).
     __device__ __forceinline__ int segments() const { return REST ? G + 2 : G; }
@@ -52,7 +56,7 @@ struct RaggedTiles {
         const int j = min(first + lane, segments());
         lo = bound(j);
         hi = max(lo, bound(min(j + 1, segments())));
-        upto = wave_scan((hi - lo + BM - 1) / BM, lane);
+        upto = wave_scan(tiles_of(hi - lo), lane);
         return __builtin_amdgcn_readlane(upto, 63);
     }
     // The number of tiles, of which `most` (below 2^24) suffice for offsets that
@@ -75,7 +79,7 @@ struct RaggedTiles {
                 const int l = __builtin_ctzll(past);
                 const int g = first + l - (REST ? 1 : 0);
                 const int begin = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
-                const int tiles = (end - begin + BM - 1) / BM;
+                const int tiles = tiles_of(end - begin);
                 const int nth = t - (__builtin_amdgcn_readlane(upto, l) - tiles);
                 // (offsets that decrease can overflow the sums of tiles)
                 if ((unsigned)nth >= (unsigned)tiles) return false;
