@@ -41,11 +41,24 @@ int launch_dense(const FusedArgs &a, bool direct, hipStream_t s) {
     return direct ? launch_epilogue<BM, BN, STAGES, EPI_SCALED>(a, s) : launch_epilogue<BM, BN, STAGES, EPI_ACT>(a, s);
 }
 
+// Workgroups of `threads` threads over `rows` rows each.  A launch holds fewer
+// than 2^32 threads; more rows take another one.
+int launch_quant_rows(void (*kernel)(QuantParams), QuantParams p, int rows, int threads, hipStream_t s) {
+    const int64_t most = ((int64_t(1) << 32) - 1) / threads * rows;
+    for (int64_t left = p.M; left > 0; left -= most) {
+        p.M = (int)(left < most ? left : most);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(p.M, rows)), dim3(threads), 0, s, p);
+        if (const int st = launch_status("row quantisation kernel")) return st;
+        p.X += most * p.ldx;
+        p.Q += most * p.ldq;
+        p.scale += most;
+    }
+    return ok();
+}
+
 template <int T, int R>
 int launch_quant(const QuantParams &p, hipStream_t s) {
-    const int rows = T < 256 ? 256 / T : 1;
-    hipLaunchKernelGGL((fp8g::quantize_rows_kernel<T, R>), dim3((unsigned)cdiv(p.M, rows)), dim3(T < 256 ? 256 : T), 0, s, p);
-    return launch_status("row quantisation kernel");
+    return launch_quant_rows(fp8g::quantize_rows_kernel<T, R>, p, T < 256 ? 256 / T : 1, T < 256 ? 256 : T, s);
 }
 
 // (the numbers of chunks that the rule of int8_quantize_rows leaves each T)
@@ -145,7 +158,7 @@ int int8_quantize_rows(const void *X, int64_t ldx, void *Q, int64_t ldq, float *
     if (ldq < K) return fail(FP8G_ERR_STRIDE, "row stride %lld of Q below K=%d", (long long)ldq, K);
     if (ldq % 16) return fail(FP8G_ERR_ALIGN, "row stride %lld of Q is not a multiple of 16 bytes", (long long)ldq);
     if ((st = check_apart({area("Q", Q, ldq, M, K, 1), area("scale", scale, M, 4)}, {area("X", X, ldx, M, K, 2)})) ||
-        (st = check_grid(M)) || (st = check_device()))
+        (st = check_device()))
         return st;
     QuantParams p = {};
     p.X = static_cast<const uint16_t *>(X);
@@ -163,8 +176,7 @@ int int8_quantize_rows(const void *X, int64_t ldx, void *Q, int64_t ldq, float *
     if (K <= 1024 || (K <= 2048 && M >= 1024)) return launch_quant_chunks<64>(p, s);
     if (K <= 8192 || (K <= 16384 && M >= 512 && M < 4096)) return launch_quant_chunks<256>(p, s);
     if (K <= 65536) return launch_quant_chunks<1024>(p, s);
-    hipLaunchKernelGGL(fp8g::quantize_long_rows_kernel, dim3((unsigned)M), dim3(1024), 0, s, p);
-    return launch_status("row quantisation kernel");
+    return launch_quant_rows(fp8g::quantize_long_rows_kernel, p, 1, 1024, s);
 }
 
 }  // extern "C"
