@@ -893,6 +893,9 @@ def grouped_gemm_ragged_int8(a, b, offsets, scale_a=None, scale_b=None, out=None
     tt = _tt()
     _int8_only(tt, a, b)
     M, G, N, K = _ragged(tt, a, b, offsets)
+    # (as many elements in another order: a scale of each channel for each expert)
+    if scale_b is not None and scale_b.dim() > 1 and G > 1 and scale_b.shape[0] == N != G:
+        raise ValueError(f"scale_b must be a [{G}, {N}] tensor, got {list(scale_b.shape)}")
     index = _device(a, b, offsets, scale_a, scale_b)
     lda = _operand(a, "a", M, K, 16)
     ldb, step = _expert_weights(b, G, N, K, 16)

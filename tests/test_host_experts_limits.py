@@ -1,5 +1,7 @@
-"""Sizes at the experts' and integer entry points' limits (CPU only: fake addresses, no kernel launch)."""
+"""Sizes at the experts' and integer entry points' limits, and shapes that hold as many elements in another order (CPU
+only: fake addresses, no kernel launch)."""
 import pytest
+import torch
 
 from tests.test_host_experts import CALLS
 from tests.test_host_fused import call, f  # noqa: F401 (f: fixture)
@@ -14,3 +16,16 @@ FAR = dict(X=at(0), Q=at(0) + (1 << 45), s=at(0) + (1 << 46))
 def test_quantise_takes_any_number_of_rows(f, M, K):  # noqa: F811
     st, msg = call(f, "int8_quantize_rows", *CALLS["int8_quantize_rows"], M=M, K=K, ldx=K, ldq=K, **FAR)
     assert st == UNSUPPORTED, msg
+
+
+def test_transposed_channel_scales_are_refused(f):  # noqa: F811
+    a, o = torch.zeros(4, 32, dtype=torch.int8), torch.zeros(3, dtype=torch.int32)
+    for N, shape in ((8, (8, 2)), (8, (8, 2, 1)), (16, (16, 2))):
+        with pytest.raises(ValueError, match="scale_b must be"):
+            f.grouped_gemm_ragged_int8(a, torch.zeros(2, N, 32, dtype=torch.int8), o, scale_b=torch.ones(shape))
+    # the same order in another shape goes on (to the check of the device)
+    for shape in ((2, 8), (16,), (16, 1), (2, 8, 1), (1, 16)):
+        with pytest.raises(ValueError, match="GPU"):
+            f.grouped_gemm_ragged_int8(a, torch.zeros(2, 8, 32, dtype=torch.int8), o, scale_b=torch.ones(shape))
+    with pytest.raises(ValueError, match="GPU"):
+        f.grouped_gemm_ragged_int8(a, torch.zeros(1, 8, 32, dtype=torch.int8), o[:2], scale_b=torch.ones(8, 1))
