@@ -16,7 +16,7 @@ int launch_sums_shape(const FusedArgs &a, const int32_t *offsets, int rows, hipS
     // next (17 of 1032 x 2056: 42.7 us, 48.1 past it).
     p.stream = (int64_t)p.G * p.M * p.N * 2 > (int64_t(256) << 20);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    if (const int st = check_grid(tiles * p.G)) return st;
+    if (const int st = check_tiles(tiles * p.G)) return st;
     const dim3 grid((unsigned)persistent_grid(tiles * p.G)), block(256);
     hipLaunchKernelGGL((fp8g::ragged_tile_kernel<BM, BN, STAGES, false, true, true, false, PLACE_SUMS, EPI_STORE>), grid,
                        block, 0, s, p);

@@ -167,9 +167,11 @@ RaggedParams<E, SCALED, PLACE> with_offsets(const FusedArgs &a, const int32_t *o
     return p;
 }
 
-// A grid of at most 2^32 threads.
-int check_grid(int64_t workgroups) {
-    if (workgroups >= (int64_t(1) << 24)) return fail(FP8G_ERR_SHAPE, "%lld workgroups: too many for one launch", (long long)workgroups);
+// The persistent kernels count their tiles in 32 bits, with room for the step
+// from one to the next.
+constexpr int64_t kMaxTiles = int64_t(1) << 30;
+int check_tiles(int64_t tiles) {
+    if (tiles > kMaxTiles) return fail(FP8G_ERR_SHAPE, "%lld tiles: too many for one launch", (long long)tiles);
     return FP8G_OK;
 }
 
@@ -181,7 +183,7 @@ int launch_rows_shape(const FusedArgs &a, const int32_t *offsets, hipStream_t s)
     auto p = with_offsets<EPI, INT, PLACE>(a, offsets);
     p.tiles_n = (int)cdiv(p.N, BN);
     const int64_t bound = tiles_bound(p.M, p.G + (PLACE == PLACE_REST ? 2 : 0), BM), wgs = bound * p.tiles_n;
-    if (const int st = check_grid(wgs)) return st;
+    if (const int st = check_tiles(wgs)) return st;
     p.tiles_m = (int)bound;
     const dim3 grid((unsigned)persistent_grid(wgs)), block(256);
     if (p.K % (INT ? 128 : 64))
@@ -202,8 +204,8 @@ int launch_rows(ShapeClass c, const FusedArgs &a, const int32_t *offsets, hipStr
 template <int RB, int CB, bool INT>
 int launch_ragged_few(const FusedArgs &a, const int32_t *offsets, hipStream_t s) {
     const auto p = with_offsets<fp8g::EPI_ACT, INT, PLACE_GROUPS>(a, offsets);
+    // (N is below 2^22 here, and pick_ragged keeps grid y below 2^16)
     const dim3 grid((unsigned)cdiv(p.N, 16 * RB), (unsigned)tiles_bound(p.M, p.G, 16 * CB)), block(256);
-    if (const int st = check_grid((int64_t)grid.x * grid.y)) return st;
     hipLaunchKernelGGL((fp8g::ragged_decode_kernel<RB, CB, INT, few_slots(RB, CB)>), grid, block, 0, s, p);
     return launch_status("ragged few-token kernel");
 }

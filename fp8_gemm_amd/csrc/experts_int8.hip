@@ -23,7 +23,8 @@ int launch_epilogue(const FusedArgs &a, hipStream_t s) {
     p.tiles_m = (int)cdiv(p.M, BM);
     p.tiles_n = (int)cdiv(p.N, BN);
     const int64_t wgs = (int64_t)p.tiles_m * p.tiles_n;
-    if (const int st = check_grid(wgs)) return st;
+    if (EPI != EPI_SCALED && wgs > kMaxWorkgroups) return fail(FP8G_ERR_SHAPE, "%lld workgroups: too many for one launch", (long long)wgs);
+    if (const int st = check_tiles(wgs)) return st;
     const dim3 grid((unsigned)(EPI == EPI_SCALED ? persistent_grid(wgs) : wgs)), block(256);
     if (p.K % 128) hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, true, EPI>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((fp8g::int8_tile_kernel<BM, BN, STAGES, false, EPI>), grid, block, 0, s, p);

@@ -155,6 +155,10 @@ FewShape few_shape(int64_t M, int64_t N, bool gated, int rb) {
     return f;
 }
 
+// A launch holds fewer than 2^32 threads along a dimension of its grid: most
+// workgroups of 256.  Classes that would need more are not chosen.
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 // The class with the smallest estimated time in us.  A tiled kernel's: a
 // launch, and per wave of 256 workgroups (one per CU) a fixed part (prologue
 // and epilogue) and its 128-byte K steps, each the slower the more CUs work
@@ -209,6 +213,7 @@ Choice pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated) {
     if (M <= kFewMaxM) {
         for (int rb = gated ? 2 : 1; rb <= 4; rb *= 2) {
             const FewShape f = few_shape(M, N, gated, rb);
+            if (f.workgroups / cdiv(M, 64) > kMaxWorkgroups) continue;
             int fit = 160 * 1024 / (kFewWaves * (f.rb + f.cb) * 2048 * few_slots(f.rb, f.cb));
             if (fit > 3) fit = 3;
             double rounds = fit == 1 ? (double)cdiv(f.workgroups, 256) : (double)f.workgroups / 256.0;
@@ -218,7 +223,9 @@ Choice pick_class(int64_t M, int64_t N, int64_t K, int unit, bool gated) {
         }
     }
     for (int c = 0; c < 3; ++c) {
-        const double t = floored(tiled_time(c, unit, cdiv(M, kClassRows[c]) * cdiv(cols, kClassCols[c]), cdiv(K * unit, 128)));
+        const int64_t wgs = cdiv(M, kClassRows[c]) * cdiv(cols, kClassCols[c]);
+        if (wgs > kMaxWorkgroups) continue;
+        const double t = floored(tiled_time(c, unit, wgs, cdiv(K * unit, 128)));
         if (t < least) least = t, best = Choice{(ShapeClass)(C_128x128 + c), {}};
     }
     return best;

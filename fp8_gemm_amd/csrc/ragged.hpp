@@ -59,7 +59,7 @@ struct RaggedTiles {
         upto = wave_scan(tiles_of(hi - lo), lane);
         return __builtin_amdgcn_readlane(upto, 63);
     }
-    // The number of tiles, of which `most` (below 2^24) suffice for offsets that
+    // The number of tiles, of which `most` (up to 2^30) suffice for offsets that
     // do not decrease.
     __device__ __forceinline__ int count(int most) {
         int n = 0;

@@ -29,3 +29,10 @@ def test_transposed_channel_scales_are_refused(f):  # noqa: F811
             f.grouped_gemm_ragged_int8(a, torch.zeros(2, 8, 32, dtype=torch.int8), o, scale_b=torch.ones(shape))
     with pytest.raises(ValueError, match="GPU"):
         f.grouped_gemm_ragged_int8(a, torch.zeros(1, 8, 32, dtype=torch.int8), o[:2], scale_b=torch.ones(8, 1))
+
+
+@pytest.mark.parametrize("m,n", [((1 << 31) - 1, 5), (1, (1 << 30) + 8), (64, (1 << 30) + 8), (1, (1 << 31) - 1)])
+def test_chosen_classes_fit_a_launch(f, m, n):  # noqa: F811
+    """A launch holds fewer than 2^32 threads along a dimension of its grid (the largest outputs that memory holds)."""
+    for p in (f.experts_plan(4, m, n, 16), f.fused_plan(0, m, n, 16), f.fused_plan(2, m, n, 16)):
+        assert p.workgroups // (-(-m // 64) if p.variant == 4 else 1) < 1 << 24, (p.variant, p.workgroups)
