@@ -35,7 +35,8 @@ int fp8_gemm_experts_plan(int op, int m, int n, int k, int groups, fp8g_plan *ou
     const int unit = op == 1 || op == 4 ? 1 : 2;
     if (const int st = op == 4 ? check_sizes(m, n, k, 1) : check_ragged_sizes(m, groups, n, k, unit)) return st;
     const bool none = op == 4 ? m == 0 || n == 0 : op == 3 ? groups == 0 || n == 0 || k == 0 : m == 0 || (op == 2 ? k == 0 : n == 0 || groups == 0);
-    if (none) return ok();
+    // (sizes that the call itself refuses: no kernel either)
+    if (none || (unit == 1 && check_int8_sizes(k)) || ((op == 2 || op == 3) && check_sum_rows(m))) return ok();
     ShapeClass c;
     int64_t tiles, cols;
     if (op == 3) {
@@ -59,10 +60,12 @@ int fp8_gemm_experts_plan(int op, int m, int n, int k, int groups, fp8g_plan *ou
         tiles = op == 4 ? cdiv(m, rows) : tiles_bound(m, groups + (op == 2 ? 2 : 0), rows);
         cols = op == 2 ? k : n;
     }
+    tiles *= cdiv(cols, kClassCols[c - C_128x128]);
+    if (tiles > (op == 4 && n % 8 ? kMaxWorkgroups : kMaxTiles)) return ok();
     out->variant = c == C_128x128 ? 7 : (c == C_128x256 ? 2 : 1);
     out->tile_m = (int)kClassRows[c - C_128x128];
     out->tile_n = (int)kClassCols[c - C_128x128];
-    out->workgroups = tiles * cdiv(cols, out->tile_n);
+    out->workgroups = tiles;
     return ok();
 }
 
@@ -92,8 +95,7 @@ int bf16_grouped_gemm_ragged_backward(const void *dD, int64_t ldg, const void *A
                                       void *stream) {
     int st;
     if ((st = check_ragged_sizes(M, G, N, K, 2))) return st;
-    // M is the weight gradients' longest sum, counted in K steps
-    if (M > (1 << 30)) return fail(FP8G_ERR_SHAPE, "M=%d exceeds %d", M, 1 << 30);
+    if ((st = check_sum_rows(M))) return st;
     const bool want_a = dA && M > 0 && K > 0, want_b = dB && G > 0 && N > 0 && K > 0;
     if (!want_a && !want_b) return ok();
     const bool sums = M > 0 && N > 0 && G > 0;       // anything to add up

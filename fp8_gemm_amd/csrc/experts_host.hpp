@@ -22,6 +22,20 @@ int check_ragged_sizes(int M, int G, int N, int K, int unit) {
     return FP8G_OK;
 }
 
+constexpr int kMaxIntK = 131056;                   // 2^14 K < 2^31
+int check_int8_sizes(int K) {
+    if (K > kMaxIntK) return fail(FP8G_ERR_SHAPE, "K=%d exceeds %d: a sum could leave 32 bits", K, kMaxIntK);
+    return FP8G_OK;
+}
+
+// Token rows of a backward pass: the weight gradients' longest sum, counted in
+// K steps.
+constexpr int kMaxSumRows = 1 << 30;
+int check_sum_rows(int M) {
+    if (M > kMaxSumRows) return fail(FP8G_ERR_SHAPE, "M=%d exceeds %d", M, kMaxSumRows);
+    return FP8G_OK;
+}
+
 // A BF16 output whose tiles are addressed with 32-bit offsets.
 int check_tile_output(const char *name, const void *ptr, int64_t ld, int cols) {
     if (const int st = check_output(name, ptr, ld, cols)) return st;

@@ -9,13 +9,6 @@ using fp8g::EPI_SCALED;
 using fp8g::FMT_I8;
 using fp8g::QuantParams;
 
-constexpr int kMaxIntK = 131056;                   // 2^14 K < 2^31
-
-int check_int8_sizes(int K) {
-    if (K > kMaxIntK) return fail(FP8G_ERR_SHAPE, "K=%d exceeds %d: a sum could leave 32 bits", K, kMaxIntK);
-    return FP8G_OK;
-}
-
 template <int BM, int BN, int STAGES, int EPI>
 int launch_epilogue(const FusedArgs &a, hipStream_t s) {
     fp8g::Int8Params<EPI> p = {};

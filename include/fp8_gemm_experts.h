@@ -28,7 +28,9 @@
  * never reads the offsets: the kernel is chosen from M and G.
  *   B: expert g's [N x K] weights begin b_stride elements after those of
  *   expert g - 1 (b_stride >= (N - 1) ldb + K and aligned as ldb is).
- *   N % 8 == 0, G <= 65535.
+ *   N % 8 == 0 and N < 2^22, G <= 65535.
+ *   At most 2^30 tiles of the chosen kernel (FP8G_ERR_SHAPE), which outputs that
+ *   fit the memory do not reach.
  */
 #ifndef FP8_GEMM_EXPERTS_H
 #define FP8_GEMM_EXPERTS_H
@@ -62,7 +64,7 @@ int bf16_grouped_gemm_ragged(const void *A, int64_t lda, const void *B, int64_t 
  *   dB[g] = bf16_rne( sum_{r of g} dD[r]^T A[r] )         [G][N][lddb], zeros for an expert without rows;
  *           expert g's begins db_stride elements after expert g - 1's
  *   Either of dA and dB may be NULL (not computed).  Rows of dD of no expert
- *   are not read.
+ *   are not read.  M at most 2^30.
  */
 int bf16_grouped_gemm_ragged_backward(const void *dD, int64_t ldg, const void *A, int64_t lda, const void *B,
                                       int64_t ldb, int64_t b_stride, const int32_t *offsets, void *dA, int64_t ldda,
@@ -109,7 +111,9 @@ int int8_quantize_rows(const void *X, int64_t ldx, void *Q, int64_t ldq, float *
  *   activation and residual (groups is not used).
  * Fills the plan of fp8_gemm.h as fp8_gemm_fused_plan does; workgroups counts
  * as many tiles as any offsets can need (the tiled kernels run them on at most
- * 256 persistent workgroups).
+ * 256 persistent workgroups).  Variant 0: nothing is launched, as there is
+ * nothing to compute or the call refuses the size (integers with K > 131056,
+ * gradients of more than 2^30 rows, more tiles than a launch holds).
  */
 int fp8_gemm_experts_plan(int op, int m, int n, int k, int groups, fp8g_plan *out);
 

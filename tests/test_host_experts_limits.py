@@ -36,3 +36,14 @@ def test_chosen_classes_fit_a_launch(f, m, n):  # noqa: F811
     """A launch holds fewer than 2^32 threads along a dimension of its grid (the largest outputs that memory holds)."""
     for p in (f.experts_plan(4, m, n, 16), f.fused_plan(0, m, n, 16), f.fused_plan(2, m, n, 16)):
         assert p.workgroups // (-(-m // 64) if p.variant == 4 else 1) < 1 << 24, (p.variant, p.workgroups)
+
+
+@pytest.mark.parametrize("op,m,n,k,g,runs", [
+    (1, 64, 64, 131056, 4, True), (1, 64, 64, 131072, 4, False), (4, 64, 64, 131056, 1, True), (4, 64, 64, 131072, 1, False),
+    (4, 3000, 5000, 131072, 1, False), (0, 64, 64, 131072, 4, True), (2, 1 << 30, 64, 64, 4, True), (2, (1 << 30) + 1, 64, 64, 4, False),
+    (3, 1 << 30, 64, 64, 4, True), (3, (1 << 30) + 1, 64, 64, 4, False), (3, 64, 4194296, 1 << 20, 8, True),
+    (3, 64, 4194296, 1 << 20, 65535, False), (0, (1 << 31) - 1, 4194296, 64, 4, False),
+])
+def test_plan_of_refused_sizes_names_no_kernel(f, op, m, n, k, g, runs):  # noqa: F811
+    p = f.experts_plan(op, m, n, k, g)
+    assert (p.variant != 0) == runs == (p.workgroups != 0)
