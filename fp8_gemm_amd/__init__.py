@@ -800,7 +800,8 @@ def gated_nt_bf16_backward(grad_out, a, w_gate, w_up, preact, activation="silu",
 
 def experts_plan(op: int, m: int, n: int, k: int, groups: int = 1) -> Plan:
     """Kernel choice of a ragged or integer form (no launch).  op: 0 grouped_gemm_ragged_bf16, 1 grouped_gemm_ragged_int8,
-    2 and 3 the token and weight gradients of grouped_gemm_ragged_bf16_backward, 4 gemm_nt_int8."""
+    2 and 3 the token and weight gradients of grouped_gemm_ragged_bf16_backward, 4 gemm_nt_int8 without activation and
+    residual.  Variant 0: nothing is launched (nothing to compute, or sizes that the call refuses)."""
     out = Plan()
     _check(load_library().fp8_gemm_experts_plan(op, m, n, k, groups, ctypes.byref(out)))
     return out
@@ -838,7 +839,8 @@ def grouped_gemm_ragged_bf16(a, b, offsets, out=None):
         out[r, n] = bf16(a[r] . b[g, n])    for offsets[g] <= r < offsets[g + 1]
 
     a: bfloat16 [M, K], the rows sorted by expert; b: bfloat16 [G, N, K] with
-    any row and expert stride; offsets: int32 [G + 1] on the GPU, not
+    any row stride, one expert's matrix behind the other's at any distance that
+    keeps them apart; offsets: int32 [G + 1] on the GPU, not
     decreasing, from 0 to M; an expert may have any number of rows.  Rows of no
     expert (before offsets[0], from offsets[G] on) are left as they were in
     `out`, unset where it is allocated here.  K % 8 == 0 and N % 8 == 0.

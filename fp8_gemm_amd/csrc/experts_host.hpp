@@ -159,8 +159,12 @@ ShapeClass pick_sums(int64_t M, int64_t G, int64_t N, int64_t K) {
     return best;
 }
 
-// The dense integer product: few tokens or not as for FP8; `direct`: the
-// tiled kernel is the persistent one.
+// The dense integer product.  Few tokens or not as for FP8, by the constants of
+// that form's tiles, which are slower than the persistent ones: between 256 and
+// 1024 rows with K of 8192 and more the few-token kernel is taken where
+// ragged_time puts the tiles up to 30% lower (not measured).  `direct`: the
+// tiled kernel is the persistent one, and its class the one with the least of
+// its own estimates; the staged form's goes by FP8's too.
 Choice pick_dense(int64_t M, int64_t N, int64_t K, bool direct) {
     Choice best = pick_class(M, N, K, 1, false);
     if (best.c == C_FEW || !direct) return best;

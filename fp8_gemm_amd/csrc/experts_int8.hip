@@ -166,7 +166,13 @@ int int8_quantize_rows(const void *X, int64_t ldx, void *Q, int64_t ldq, float *
     // 1024 threads): 512 x 1024 values 2.56 | 2.69 | 3.37, 64 x 2048 2.87 | 2.57 |
     // 2.66, 8192 x 2048 9.8 | 10.9 | 24, 256 x 4096 3.57 | 2.82 | 2.91, 2048 x 8192
     // - | 9.4 | 12.7, 64 x 14336 - | 3.62 | 3.35, 1024 x 14336 - | 8.6 | 9.1, 8192 x
-    // 14336 - | 65.2 | 60.9.
+    // 14336 - | 65.2 | 60.9.  On another box, three inputs in turn, 256 | 1024
+    // threads: 512 x 10240 4.65 | 5.16, 2048 x 10240 11.6 | 13.3, 4096 x 10240 21.3 |
+    // 23.7, 256 x 12288 3.70 | 3.66, 1024 x 12288 8.97 | 9.16, 4096 x 12288 25.1 |
+    // 25.6, 8192 x 12288 50.1 | 47.1, 256 x 16384 4.20 | 3.94, 512 x 16384 7.26 |
+    // 7.06, 2048 x 16384 16.9 | 17.6, 4096 x 16384 32.6 | 34.0, 8192 x 16384 73.8 |
+    // 70.0: what is taken is within 5% of the other but for 4096 and more rows of
+    // about 10000 values (7 to 12%).
     if (K <= 1024 || (K <= 2048 && M >= 1024)) return launch_quant_chunks<64>(p, s);
     if (K <= 8192 || (K <= 16384 && M >= 512 && M < 4096)) return launch_quant_chunks<256>(p, s);
     if (K <= 65536) return launch_quant_chunks<1024>(p, s);

@@ -33,8 +33,10 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
 }
 
 // The tiles of BM rows of all experts, in order of their rows.  Each wave
-// works on its own, a lane per expert, 64 experts at a time; with up to 64
-// (the usual number) the offsets are read once.
+// works on its own, a lane per segment (an expert; with REST also the rows
+// before the first and behind the last of them), 64 segments at a time.  Up to
+// 64 segments (64 experts, or 62 with REST) are read once; more are read again,
+// a batch of 64 after the other, for every tile that is looked for.
 template <int BM, bool REST>
 struct RaggedTiles {
     const int32_t *offsets;

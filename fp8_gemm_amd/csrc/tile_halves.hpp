@@ -58,7 +58,7 @@ namespace fp8g {
 // CU, each on tiles blockIdx.x, + gridDim.x, ..., so that the number of tiles
 // need not be known to the host.  A tile's first copies go out before the
 // tile before it is written, which hides their way from memory, the launch and
-// the offsets behind the epilogue.  Tiles of at most BM / 2 rows (an expert's
+// most of the offsets' loads behind the epilogue.  Tiles of at most BM / 2 rows (an expert's
 // last rows, the cut tiles of the last round) run a step of half the matrix
 // instructions, which takes about 0.7 of a whole one's time: 4096 x 14336 x 4096
 // in 8-bit integers, 3.5 rounds, 196 -> 189 us; 2048 x 4096 x 14336, half a
@@ -492,7 +492,10 @@ __device__ __forceinline__ void tile_halves_body(P p) {
             else vmcnt_wait<CPW * (STAGES - 1) + STORES>();
             t += gridDim.x;
             Where next;
-            const bool more = __builtin_amdgcn_readfirstlane(place(t, next));   // (its loads, if any, before the loop)
+            // (the offsets of more than 64 segments are loaded here, before the
+            // loop, and waited for with the copies at hand; a weight gradient's
+            // two offsets behind it, in aim)
+            const bool more = __builtin_amdgcn_readfirstlane(place(t, next));
             sum(acc);
             uint16_t *const out = d + (int64_t)m0 * p.ldd + n0;
             const int rows = rows_m, col0 = n0;
